@@ -10,8 +10,10 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # The in-tree build; CKL_LIBRARY names another build of the same library.
@@ -91,6 +93,21 @@ def lib() -> ctypes.CDLL:
                                         ctypes.c_int),
         "ckl_topk_cache_vocab_parallel": ([_P, ctypes.POINTER(_VocabGroupC), _P, _P, _I64, _I64,
                                            _P, _P, _P, _SZ, _P, ctypes.c_int], ctypes.c_int),
+        "ckl_embed": ([_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_float, _P, _P, ctypes.c_int],
+                      ctypes.c_int),
+        "ckl_embed_vp_workspace_bytes": ([_P, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
+        "ckl_embed_vocab_parallel": ([_P, ctypes.POINTER(_VocabGroupC), _P, _P, _P, _I64,
+                                      ctypes.c_float, _P, _P, _SZ, _P, ctypes.c_int], ctypes.c_int),
+        "ckl_embed_grad_workspace_bytes": ([_P, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
+        "ckl_embed_grad": ([_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_float, ctypes.c_int, _P, _P,
+                            _SZ, _P, ctypes.c_int], ctypes.c_int),
+        "ckl_act8_pack": ([_P, _P, _I64, _I64, ctypes.c_int, _P, _P, _P], ctypes.c_int),
+        "ckl_act8_unpack": ([_P, _P, _P, _I64, _I64, ctypes.c_int, _P, _P], ctypes.c_int),
+        "ckl_norm": ([_P, _P, _P, _P, _I64, ctypes.c_float, ctypes.c_int, _P, _P, _P, _P, _P, _P],
+                     ctypes.c_int),
+        "ckl_norm_bwd_workspace_bytes": ([_P, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
+        "ckl_norm_bwd": ([_P, _P, _P, _P, _P, _P, _P, _I64, ctypes.c_int, ctypes.c_int, _P, _P, _P,
+                          _SZ, _P], ctypes.c_int),
         "ckl_profile_enable": ([_P, ctypes.c_int, ctypes.c_int], ctypes.c_int),
         "ckl_profile_collect": ([_P, ctypes.POINTER(KernelStat), ctypes.c_int,
                                  ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
@@ -196,6 +213,35 @@ def torch_vocab_group(V_total: int, group=None) -> VocabGroup:
     return VocabGroup(world, rank, V_total, v0,
                       lambda send, recv: dist.all_gather_into_tensor(recv, send, group=group),
                       lambda buf: dist.all_reduce(buf, group=group))
+
+
+ACT8_FORMATS = {"int8": 0, "e4m3": 1}
+
+
+class Act8:
+    """An 8-bit activation checkpoint: codes q (T x cols, uint8), one power-of-two scale per
+    32 columns of a row (T x ceil(cols / 32), uint8: exponent + 127, 255 for a block that held
+    an infinity or a NaN) and, from a norm, the rows' factors rstd (T, float32)."""
+
+    def __init__(self, q, scale, fmt: str = "int8", rstd=None):
+        if fmt not in ACT8_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(ACT8_FORMATS)}")
+        if q.dtype != torch.uint8 or scale.dtype != torch.uint8:
+            raise TypeError("q and scale must be uint8")
+        if q.dim() != 2 or q.shape[1] == 0 or \
+                tuple(scale.shape) != (q.shape[0], (q.shape[1] + 31) // 32):
+            raise ValueError("q must be T x cols and scale T x ceil(cols / 32)")
+        if rstd is not None and (rstd.dtype != torch.float32 or tuple(rstd.shape) != (q.shape[0],)):
+            raise TypeError("rstd must be a float32 tensor of T entries")
+        for t in (q, scale) + ((rstd,) if rstd is not None else ()):
+            if not t.is_contiguous() or t.device != q.device:
+                raise ValueError("q, scale and rstd must be contiguous tensors on one device")
+        self.q, self.scale, self.fmt, self.rstd = q, scale, fmt, rstd
+
+    @property
+    def nbytes(self) -> int:
+        return self.q.numel() + self.scale.numel() + \
+            (4 * self.rstd.numel() if self.rstd is not None else 0)
 
 
 class ChunkedKL:
@@ -446,6 +492,193 @@ class ChunkedKL:
         _check(code, "ckl_topk_cache_vocab_parallel")
         return idx, logit
 
+    # ------------------------------------------------------------------ operators around the loss
+    def _dense(self, *tensors):
+        for t in tensors:
+            if t is not None and (not t.is_contiguous() or t.device != self.device):
+                raise ValueError("inputs must be contiguous tensors on the handle's device")
+
+    def _rows(self, name, t, shape=None):
+        if t.dtype != self.dtype:
+            raise TypeError(f"{name} must be {self.dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have the shape {tuple(shape)}")
+        self._dense(t)
+
+    def _ids(self, ids, mask):
+        if ids.dtype != torch.int32:
+            raise TypeError("ids must be int32")
+        if mask is not None and (mask.dtype != torch.uint8 or mask.numel() != ids.numel()):
+            raise TypeError("mask must be a uint8 tensor with an entry for each id")
+        self._dense(ids, mask)
+
+    def _workspace(self, query, *args) -> torch.Tensor:
+        n = _SZ()
+        _check(getattr(lib(), query)(self._h, *args, ctypes.byref(n)), query)
+        return torch.empty(n.value, dtype=torch.uint8, device=self.device)
+
+    def _stream(self, stream):
+        s = stream or torch.cuda.current_stream(self.device)
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def embed(self, ids, W, mask=None, scale: float = 1.0, V_total: int | None = None, v0: int = 0,
+              out=None, sync: bool = True, stream=None):
+        """scale * W[ids - v0] in the handle's dtype (ids' shape, then d): zeros for tokens with
+        mask 0 and for ids in [0, V_total) whose row is not among the handle's V (v0 ..)."""
+        self._ids(ids, mask)
+        self._rows("W", W, (self.V, self.d))
+        shape = tuple(ids.shape) + (self.d,)
+        if out is None:
+            out = torch.empty(shape, dtype=self.dtype, device=self.device)
+        self._rows("out", out, shape)
+        _check(lib().ckl_embed(self._h, _ptr(ids), _ptr(mask), _ptr(W), ids.numel(),
+                               self.V if V_total is None else V_total, v0, scale, _ptr(out),
+                               self._stream(stream), int(sync)), "ckl_embed")
+        return out
+
+    def embed_vocab_parallel(self, group: VocabGroup, ids, W_shard, mask=None, scale: float = 1.0,
+                             sync: bool = True, stream=None):
+        """As embed with W split by vocabulary rows over `group`: the full rows on every rank
+        (one all-reduce)."""
+        self._ids(ids, mask)
+        self._rows("W_shard", W_shard, (self.V, self.d))
+        out = torch.empty(tuple(ids.shape) + (self.d,), dtype=self.dtype, device=self.device)
+        ws = self._workspace("ckl_embed_vp_workspace_bytes", ids.numel())
+        g, keep = group._c(self.device)
+        group.error = None
+        code = lib().ckl_embed_vocab_parallel(self._h, ctypes.byref(g), _ptr(ids), _ptr(mask),
+                                              _ptr(W_shard), ids.numel(), scale, _ptr(out),
+                                              _ptr(ws), ws.numel(), self._stream(stream), int(sync))
+        del keep
+        if code == 9 and group.error is not None:
+            raise CKLError(code, "ckl_embed_vocab_parallel") from group.error
+        _check(code, "ckl_embed_vocab_parallel")
+        return out
+
+    def embed_grad(self, ids, dX, mask=None, scale: float = 1.0, V_total: int | None = None,
+                   v0: int = 0, dW=None, accumulate: bool = False, workspace=None,
+                   sync: bool = True, stream=None):
+        """dW (V x d, float32) of embed: the given buffer, added to with accumulate=True (a tied
+        head's dW from fwd_bwd) and overwritten otherwise, or a new one."""
+        self._ids(ids, mask)
+        self._rows("dX", dX, tuple(ids.shape) + (self.d,))
+        if dW is None:
+            if accumulate:
+                raise ValueError("accumulate needs dW")
+            dW = torch.empty((self.V, self.d), dtype=torch.float32, device=self.device)
+        self._f32("dW", dW, (self.V, self.d))
+        ws = workspace if workspace is not None else \
+            self._workspace("ckl_embed_grad_workspace_bytes", ids.numel())
+        _check(lib().ckl_embed_grad(self._h, _ptr(ids), _ptr(mask), _ptr(dX), ids.numel(),
+                                    self.V if V_total is None else V_total, v0, scale,
+                                    int(accumulate), _ptr(dW), _ptr(ws), ws.numel(),
+                                    self._stream(stream), int(sync)), "ckl_embed_grad")
+        return dW
+
+    def _f32(self, name, t, shape):
+        if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape):
+            raise TypeError(f"{name} must be a float32 tensor of shape {tuple(shape)}")
+        self._dense(t)
+
+    def _act8(self, ckpt: Act8, cols=None):
+        self._dense(ckpt.q, ckpt.scale, ckpt.rstd)
+        if cols is not None and ckpt.q.shape[1] != cols:
+            raise ValueError(f"the checkpoint must have {cols} columns")
+        return ACT8_FORMATS[ckpt.fmt]
+
+    def _new_act8(self, T, cols, fmt, rstd):
+        return Act8(torch.empty((T, cols), dtype=torch.uint8, device=self.device),
+                    torch.empty((T, (cols + 31) // 32), dtype=torch.uint8, device=self.device), fmt,
+                    torch.empty(T, dtype=torch.float32, device=self.device) if rstd else None)
+
+    def act8_pack(self, x, fmt: str = "int8", out: Act8 | None = None, stream=None) -> Act8:
+        """The 8-bit checkpoint of x (T x cols, any cols that is a multiple of 8)."""
+        if x.dim() != 2:
+            raise ValueError("x must be T x cols")
+        self._rows("x", x)
+        ckpt = out if out is not None else self._new_act8(x.shape[0], x.shape[1], fmt, False)
+        f = self._act8(ckpt, x.shape[1])
+        if ckpt.q.shape[0] != x.shape[0]:
+            raise ValueError("the checkpoint must have a row for each row of x")
+        _check(lib().ckl_act8_pack(self._h, _ptr(x), x.shape[0], x.shape[1], f, _ptr(ckpt.q),
+                                   _ptr(ckpt.scale), self._stream(stream)), "ckl_act8_pack")
+        return ckpt
+
+    def act8_unpack(self, ckpt: Act8, out=None, stream=None):
+        """The values of a checkpoint (T x cols, the handle's dtype)."""
+        f = self._act8(ckpt)
+        if out is None:
+            out = torch.empty(tuple(ckpt.q.shape), dtype=self.dtype, device=self.device)
+        self._rows("out", out, ckpt.q.shape)
+        _check(lib().ckl_act8_unpack(self._h, _ptr(ckpt.q), _ptr(ckpt.scale), *ckpt.q.shape, f,
+                                     _ptr(out), self._stream(stream)), "ckl_act8_unpack")
+        return out
+
+    def norm(self, x, gain, residual=None, eps: float = 1e-5, checkpoint: str | None = "int8",
+             out=None, stream=None):
+        """(y, s, checkpoint): s = x + residual (x itself without one), y = s / rms(s) * gain and
+        the 8-bit checkpoint of s with the rows' factors, all that norm_bwd needs (None for
+        checkpoint=None). out = (y, s, checkpoint): buffers to write to instead of new ones
+        (s only with a residual, and it may be x's or residual's)."""
+        T = x.shape[0]
+        self._rows("x", x, (T, self.d))
+        self._rows("gain", gain, (self.d,))
+        if residual is not None:
+            self._rows("residual", residual, (T, self.d))
+        if checkpoint is not None and checkpoint not in ACT8_FORMATS:
+            raise ValueError(f"checkpoint must be None or one of {sorted(ACT8_FORMATS)}")
+        if out is None:
+            y = torch.empty_like(x)
+            s = torch.empty_like(x) if residual is not None else x
+            ckpt = self._new_act8(T, self.d, checkpoint, True) if checkpoint else None
+        else:
+            y, s, ckpt = out
+            self._rows("out[0]", y, (T, self.d))
+            if residual is not None:
+                self._rows("out[1]", s, (T, self.d))
+            else:
+                s = x
+            if (ckpt is None) != (checkpoint is None):
+                raise ValueError("out[2] must be an Act8 where a checkpoint is asked for")
+            if ckpt is not None and (ckpt.fmt != checkpoint or ckpt.rstd is None or
+                                     ckpt.q.shape[0] != T):
+                raise ValueError("out[2] must be a checkpoint of T rows with rstd in that format")
+        f = self._act8(ckpt, self.d) if ckpt is not None else 0
+        _check(lib().ckl_norm(self._h, _ptr(x), _ptr(residual), _ptr(gain), T, eps, f,
+                              _ptr(s) if residual is not None else None, _ptr(y),
+                              *((_ptr(ckpt.q), _ptr(ckpt.scale), _ptr(ckpt.rstd)) if ckpt is not None
+                                else (None, None, None)), self._stream(stream)), "ckl_norm")
+        return y, s, ckpt
+
+    def norm_bwd(self, dY, ckpt: Act8, gain, d_residual=None, dX=None, dgain=None,
+                 accumulate: bool = False, workspace=None, stream=None):
+        """(dX, dgain) of norm from its checkpoint: dX (T x d) is the gradient of x and of
+        residual, d_residual the gradient that reaches s other than through y; dgain (d,
+        float32) is added to with accumulate=True."""
+        T = ckpt.q.shape[0]
+        f = self._act8(ckpt, self.d)
+        if ckpt.rstd is None:
+            raise ValueError("the checkpoint has no rstd: it is not one of a norm")
+        self._rows("dY", dY, (T, self.d))
+        self._rows("gain", gain, (self.d,))
+        if d_residual is not None:
+            self._rows("d_residual", d_residual, (T, self.d))
+        if dX is None:
+            dX = torch.empty_like(dY)
+        self._rows("dX", dX, (T, self.d))
+        if dgain is None:
+            if accumulate:
+                raise ValueError("accumulate needs dgain")
+            dgain = torch.empty(self.d, dtype=torch.float32, device=self.device)
+        self._f32("dgain", dgain, (self.d,))
+        ws = workspace if workspace is not None else \
+            self._workspace("ckl_norm_bwd_workspace_bytes", T)
+        _check(lib().ckl_norm_bwd(self._h, _ptr(dY), _ptr(ckpt.q), _ptr(ckpt.scale), _ptr(ckpt.rstd),
+                                  _ptr(gain), _ptr(d_residual), T, f, int(accumulate), _ptr(dX),
+                                  _ptr(dgain), _ptr(ws), ws.numel(), self._stream(stream)),
+               "ckl_norm_bwd")
+        return dX, dgain
+
     def fwd_bwd_from_host(self, H_host, idx_host, logit_host, mask_host, staging, W, chunk,
                           out, workspace, stream=None) -> float:
         """Fused loss with the per-step inputs in (pinned) host memory; returns the loss.
@@ -547,6 +780,91 @@ def chunked_kl_loss(H, W, idx, logit, mask=None, chunk=None, handle: ChunkedKL |
     if group is not None:
         return _VocabParallelKLFn.apply(H, W, idx, logit, mask, handle, chunk, group, check)
     return _ChunkedKLFn.apply(H, W, idx, logit, mask, handle, chunk, check)
+
+
+_OP_HANDLES = threading.local()  # a handle must not be used by two calls at once
+
+
+def operator_handle(t, V: int = 1) -> ChunkedKL:
+    """The calling thread's cached handle for t's device and dtype, with d = t's last dimension
+    and V rows of W: for the calls that need no teacher cache (embed, act8_*, norm*)."""
+    if t.device.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    cache = _OP_HANDLES.__dict__.setdefault("handles", {})
+    key = (t.device.index, t.dtype, V, t.shape[-1])
+    h = cache.get(key)
+    if h is None:
+        h = cache[key] = ChunkedKL(V, t.shape[-1], 1, dtype=t.dtype, max_chunk=1, device=t.device)
+    return h
+
+
+class _EmbeddingFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, W, ids, mask, scale, handle, check):
+        ctx.save_for_backward(ids, mask)
+        ctx.w_dtype, ctx.scale, ctx.handle, ctx.check = W.dtype, scale, handle, check
+        return handle.embed(ids, W.detach(), mask, scale, sync=False)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        ids, mask = ctx.saved_tensors
+        dW = None
+        if ctx.needs_input_grad[0]:
+            dW = ctx.handle.embed_grad(ids, g.contiguous(), mask, ctx.scale,
+                                       sync=ctx.check).to(ctx.w_dtype)
+        elif ctx.check:
+            ctx.handle.sync_status()
+        return dW, None, None, None, None, None
+
+
+def embedding(ids, W, mask=None, scale: float = 1.0, handle: ChunkedKL | None = None,
+              check: bool = True):
+    """Autograd-friendly scale * W[ids] (zeros, and no gradient, for tokens with mask 0). W's
+    gradient is formed in fp32 by sorted tokens and does not change from run to run.
+
+    check=True: backward() waits and raises CKLError if an id was outside [0, V); check=False:
+    nothing waits and the status stays in the handle (operator_handle(W, W.shape[0]))."""
+    if handle is None:
+        handle = operator_handle(W, W.shape[0])
+    return _EmbeddingFn.apply(W, ids, mask, scale, handle, check)
+
+
+class _RmsNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gain, residual, eps, fmt, handle):
+        flat = x.detach().view(-1, handle.d)
+        res = None if residual is None else residual.detach().view(-1, handle.d)
+        y, s, ckpt = handle.norm(flat, gain.detach(), res, eps, fmt)
+        ctx.save_for_backward(ckpt.q, ckpt.scale, ckpt.rstd, gain)
+        ctx.fmt, ctx.handle, ctx.has_residual = fmt, handle, residual is not None
+        ctx.set_materialize_grads(False)
+        return y.view(x.shape) if residual is None else (y.view(x.shape), s.view(x.shape))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dY, d_sum=None):
+        q, scale, rstd, gain = ctx.saved_tensors
+        if dY is None:  # only s was used
+            return d_sum, None, d_sum if ctx.has_residual else None, None, None, None
+        h = ctx.handle
+        flat = [None if g is None else g.contiguous().view(-1, h.d) for g in (dY, d_sum)]
+        dX, dgain = h.norm_bwd(flat[0], Act8(q, scale, ctx.fmt, rstd), gain.detach(), flat[1])
+        dX = dX.view(dY.shape)
+        return dX, dgain.to(gain.dtype), dX if ctx.has_residual else None, None, None, None
+
+
+def rms_norm(x, gain, residual=None, eps: float = 1e-5, fmt: str = "int8",
+             handle: ChunkedKL | None = None):
+    """Autograd-friendly RMS norm over the last dimension; with `residual` returns (y, s) with
+    s = x + residual. What is kept for the backward pass is the 8-bit checkpoint of s (fmt) and
+    one float per row; the gradients are those of the norm at the checkpoint's values."""
+    if handle is None:
+        handle = operator_handle(x)
+    if not x.is_contiguous() or (residual is not None and
+                                 (not residual.is_contiguous() or residual.shape != x.shape)):
+        raise ValueError("x and residual must be contiguous tensors of one shape")
+    return _RmsNormFn.apply(x, gain, residual, eps, fmt, handle)
 
 
 def forward_static(H, W, idx, logit, mask=None, chunk: int = 2048, stream=None,

@@ -1,0 +1,290 @@
+// C ABI of the operators around the loss: the embedding (the other end of a tied LM
+// head), 8-bit activation checkpoints, and the RMS norm that keeps its input in one.
+// Argument checks, workspace plans and launches; the kernels are in k_embed.cu and
+// k_act8.cu.
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+
+#include "ctx.h"
+#include "k_ops.h"
+#include "kernels.h"
+
+using namespace ckl;
+
+namespace {
+
+ckl_status cuda_status(cudaError_t err) {
+  if (err == cudaSuccess) return CKL_OK;
+  std::fprintf(stderr, "ckl: CUDA error: %s\n", cudaGetErrorString(err));
+  return CKL_ERR_CUDA;
+}
+
+size_t elem(const ckl_ctx* h) { return h->dtype == CKL_BF16 ? 2 : 4; }
+
+// ------------------------------------------------------------------ embedding
+ckl_status check_ids(const ckl_ctx* h, const int32_t* ids, int64_t T, int64_t V_total, int64_t v0,
+                     float scale) {
+  if (!h || T < 0 || (T > 0 && !ids)) return CKL_ERR_INVALID_ARG;
+  if (v0 < 0 || V_total > INT32_MAX || v0 + h->V > V_total || !std::isfinite(scale))
+    return CKL_ERR_INVALID_ARG;
+  if (T > INT32_MAX) return CKL_ERR_UNSUPPORTED;
+  if (ids && !aligned(ids, 4)) return CKL_ERR_ALIGNMENT;
+  return CKL_OK;
+}
+
+EmbedIds ids_of(const ckl_ctx* h, const int32_t* ids, const uint8_t* mask, int64_t T,
+                int64_t V_total, int64_t v0) {
+  return EmbedIds{ids, mask, T, (int32_t)V_total, (int32_t)v0, (int32_t)h->V, h->d_status};
+}
+
+struct EmbedGradPlan {
+  int tile = 0;
+  size_t off_a = 0, off_b = 0, off_part = 0, total = 0;
+};
+
+EmbedGradPlan embed_grad_plan(const ckl_ctx* h, int64_t T) {
+  EmbedGradPlan p;
+  p.tile = embed_tile(T, (int)h->d, h->num_sms);
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
+  p.off_a = take((size_t)T * 8);
+  p.off_b = take((size_t)T * 8);
+  p.off_part = take((size_t)((T + p.tile - 1) / p.tile) * 2 * h->d * 4);
+  p.total = o;
+  return p;
+}
+
+// ------------------------------------------------------------------ 8-bit checkpoints
+ckl_status check_act8(const ckl_ctx* h, int64_t T, int64_t cols, int fmt, const void* q,
+                      const void* scale) {
+  if (!h || T < 0 || cols < 1 || (fmt != CKL_ACT8_INT8 && fmt != CKL_ACT8_E4M3))
+    return CKL_ERR_INVALID_ARG;
+  if (cols % 8 != 0 || cols > (1 << 20) || T > INT32_MAX) return CKL_ERR_UNSUPPORTED;
+  if (T > 0 && (!q || !scale)) return CKL_ERR_INVALID_ARG;
+  if (q && !aligned(q, 16)) return CKL_ERR_ALIGNMENT;
+  return CKL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ckl_status ckl_embed(ckl_handle h, const int32_t* ids, const uint8_t* mask, const void* W,
+                     int64_t T, int64_t V_total, int64_t v0, float scale, void* out, void* stream,
+                     int wait) {
+  ckl_status st = check_ids(h, ids, T, V_total, v0, scale);
+  if (st != CKL_OK) return st;
+  if (!W || (T > 0 && !out)) return CKL_ERR_INVALID_ARG;
+  if (!aligned(W, 16) || (out && !aligned(out, 16))) return CKL_ERR_ALIGNMENT;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return CKL_ERR_CUDA;
+  cudaGetLastError();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T > 0) {
+    Launcher L{h, s};
+    st = cuda_status(L(KID_EMBED, 0, (double)T * h->d * 2 * elem(h), [&] {
+      launch_embed(ids_of(h, ids, mask, T, V_total, v0), h->dtype == CKL_BF16, W, (int)h->d, scale,
+                   out, false, s);
+    }));
+    if (st != CKL_OK) return st;
+  }
+  return wait ? sync_and_read(h, s, nullptr, nullptr) : CKL_OK;
+}
+
+ckl_status ckl_embed_vp_workspace_bytes(ckl_handle h, int64_t T, size_t* bytes) {
+  if (!h || !bytes || T < 0) return CKL_ERR_INVALID_ARG;
+  *bytes = align_up((size_t)T * h->d * 4, 256);
+  return CKL_OK;
+}
+
+ckl_status ckl_embed_vocab_parallel(ckl_handle h, const ckl_vocab_group* g, const int32_t* ids,
+                                    const uint8_t* mask, const void* W_shard, int64_t T,
+                                    float scale, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream, int wait) {
+  if (!h || !g || g->world < 1 || g->rank < 0 || g->rank >= g->world || !g->all_reduce_sum)
+    return CKL_ERR_INVALID_ARG;
+  if (h->dtype != CKL_BF16) return CKL_ERR_UNSUPPORTED;
+  ckl_status st = check_ids(h, ids, T, g->V_total, g->v0, scale);
+  if (st != CKL_OK) return st;
+  if (!W_shard || (T > 0 && !out)) return CKL_ERR_INVALID_ARG;
+  if (!aligned(W_shard, 16) || (out && !aligned(out, 16))) return CKL_ERR_ALIGNMENT;
+  const size_t need = align_up((size_t)T * h->d * 4, 256);
+  if (T > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+    return CKL_ERR_WORKSPACE;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return CKL_ERR_CUDA;
+  cudaGetLastError();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T > 0) {
+    Launcher L{h, s};
+    float* buf = static_cast<float*>(workspace);
+    // one rank's row and zeros from the others: the sum is exact in any order
+    cudaError_t err = L(KID_EMBED, 0, (double)T * h->d * 6, [&] {
+      launch_embed(ids_of(h, ids, mask, T, g->V_total, g->v0), true, W_shard, (int)h->d, scale, buf,
+                   true, s);
+    });
+    // made even after a failed launch: the ranks' calls stay matched
+    const int rc = L.collective(KID_VP_REDUCE, (double)T * h->d * 4,
+                                [&] { return g->all_reduce_sum(g->user, buf, T * h->d, s); });
+    if (err == cudaSuccess && rc == 0)
+      err = L(KID_TO_BF16, 0, (double)T * h->d * 6, [&] {
+        launch_f32_to_bf16(buf, T * h->d, static_cast<uint16_t*>(out), s);
+      });
+    if ((st = cuda_status(err)) != CKL_OK) return st;
+    if (rc != 0) return CKL_ERR_COLLECTIVE;
+  }
+  return wait ? sync_and_read(h, s, nullptr, nullptr) : CKL_OK;
+}
+
+ckl_status ckl_embed_grad_workspace_bytes(ckl_handle h, int64_t T, size_t* bytes) {
+  if (!h || !bytes || T < 0) return CKL_ERR_INVALID_ARG;
+  *bytes = embed_grad_plan(h, T).total;
+  return CKL_OK;
+}
+
+ckl_status ckl_embed_grad(ckl_handle h, const int32_t* ids, const uint8_t* mask, const void* dX,
+                          int64_t T, int64_t V_total, int64_t v0, float scale, int accumulate,
+                          float* dW, void* workspace, size_t workspace_bytes, void* stream,
+                          int wait) {
+  ckl_status st = check_ids(h, ids, T, V_total, v0, scale);
+  if (st != CKL_OK) return st;
+  if (!dW || (T > 0 && !dX)) return CKL_ERR_INVALID_ARG;
+  if (!aligned(dW, 16) || (dX && !aligned(dX, 16))) return CKL_ERR_ALIGNMENT;
+  const EmbedGradPlan P = embed_grad_plan(h, T);
+  if (T > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < P.total))
+    return CKL_ERR_WORKSPACE;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return CKL_ERR_CUDA;
+  cudaGetLastError();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err = cudaSuccess;
+  auto chk = [&](cudaError_t e) { if (e != cudaSuccess && err == cudaSuccess) err = e; };
+  const int d = (int)h->d, V = (int)h->V;
+  if (!accumulate) chk(cudaMemsetAsync(dW, 0, (size_t)V * d * 4, s));
+  if (T > 0) {
+    unsigned char* base = static_cast<unsigned char*>(workspace);
+    uint64_t* a = reinterpret_cast<uint64_t*>(base + P.off_a);
+    uint64_t* b = reinterpret_cast<uint64_t*>(base + P.off_b);
+    float* part = reinterpret_cast<float*>(base + P.off_part);
+    const uint64_t* sorted = embed_sort_result(V) ? b : a;
+    Launcher L{h, s};
+    chk(L(KID_EMBED_SORT, 0, (double)T * 12, [&] {
+      chk(launch_embed_sort(ids_of(h, ids, mask, T, V_total, v0), a, b, s));
+    }));
+    chk(L(KID_EMBED_GRAD, 0, (double)T * d * elem(h), [&] {
+      launch_embed_grad(sorted, T, V, h->dtype == CKL_BF16, dX, d, P.tile, scale, accumulate != 0,
+                        dW, part, s);
+    }));
+    chk(L(KID_EMBED_JOIN, 0, 0, [&] {
+      launch_embed_join(sorted, T, V, d, P.tile, scale, accumulate != 0, dW, part, s);
+    }));
+  }
+  if ((st = cuda_status(err)) != CKL_OK) return st;
+  return wait ? sync_and_read(h, s, nullptr, nullptr) : CKL_OK;
+}
+
+ckl_status ckl_act8_pack(ckl_handle h, const void* X, int64_t T, int64_t cols, ckl_act8_format fmt,
+                         void* q, uint8_t* scale, void* stream) {
+  ckl_status st = check_act8(h, T, cols, fmt, q, scale);
+  if (st != CKL_OK) return st;
+  if (T > 0 && !X) return CKL_ERR_INVALID_ARG;
+  if (X && !aligned(X, 16)) return CKL_ERR_ALIGNMENT;
+  if (T == 0) return CKL_OK;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return CKL_ERR_CUDA;
+  cudaGetLastError();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Launcher L{h, s};
+  return cuda_status(L(KID_ACT8_PACK, 0, (double)T * cols * (elem(h) + 33.0 / 32), [&] {
+    launch_act8_pack(h->dtype == CKL_BF16, X, T, (int)cols, fmt, static_cast<uint8_t*>(q), scale, s);
+  }));
+}
+
+ckl_status ckl_act8_unpack(ckl_handle h, const void* q, const uint8_t* scale, int64_t T,
+                           int64_t cols, ckl_act8_format fmt, void* out, void* stream) {
+  ckl_status st = check_act8(h, T, cols, fmt, q, scale);
+  if (st != CKL_OK) return st;
+  if (T > 0 && !out) return CKL_ERR_INVALID_ARG;
+  if (out && !aligned(out, 16)) return CKL_ERR_ALIGNMENT;
+  if (T == 0) return CKL_OK;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return CKL_ERR_CUDA;
+  cudaGetLastError();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Launcher L{h, s};
+  return cuda_status(L(KID_ACT8_UNPACK, 0, (double)T * cols * (elem(h) + 33.0 / 32), [&] {
+    launch_act8_unpack(h->dtype == CKL_BF16, static_cast<const uint8_t*>(q), scale, T, (int)cols,
+                       fmt, out, s);
+  }));
+}
+
+ckl_status ckl_norm(ckl_handle h, const void* X, const void* residual, const void* gain, int64_t T,
+                    float eps, ckl_act8_format fmt, void* sum, void* Y, void* q, uint8_t* scale,
+                    float* rstd, void* stream) {
+  if (!h || T < 0 || !gain || !(eps > 0.f) || !std::isfinite(eps)) return CKL_ERR_INVALID_ARG;
+  if (fmt != CKL_ACT8_INT8 && fmt != CKL_ACT8_E4M3) return CKL_ERR_INVALID_ARG;
+  if (T > INT32_MAX) return CKL_ERR_UNSUPPORTED;
+  if (T > 0 && (!X || !Y || (residual && !sum))) return CKL_ERR_INVALID_ARG;
+  if ((q != nullptr) != (scale != nullptr) || (T > 0 && q && !rstd)) return CKL_ERR_INVALID_ARG;
+  if (residual && sum == Y && T > 0) return CKL_ERR_INVALID_ARG;
+  for (const void* p : {X, residual, gain, (const void*)sum, (const void*)Y, (const void*)q})
+    if (p && !aligned(p, 16)) return CKL_ERR_ALIGNMENT;
+  if (rstd && !aligned(rstd, 4)) return CKL_ERR_ALIGNMENT;
+  if (T == 0) return CKL_OK;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return CKL_ERR_CUDA;
+  cudaGetLastError();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  NormArgs a{};
+  a.x = X; a.res = residual; a.gain = gain; a.T = T; a.d = (int)h->d; a.eps = eps; a.fmt = fmt;
+  a.sum = sum; a.y = Y; a.q = static_cast<uint8_t*>(q); a.e = scale; a.rstd = rstd;
+  Launcher L{h, s};
+  const double per = elem(h) * (residual ? 4.0 : 2.0) + (q ? 33.0 / 32 : 0.0);
+  return cuda_status(L(KID_NORM_FWD, 0, (double)T * h->d * per, [&] {
+    launch_norm_fwd(a, h->dtype == CKL_BF16, s);
+  }));
+}
+
+ckl_status ckl_norm_bwd_workspace_bytes(ckl_handle h, int64_t T, size_t* bytes) {
+  if (!h || !bytes || T < 0) return CKL_ERR_INVALID_ARG;
+  *bytes = (size_t)norm_part_rows(T, (int)h->d, h->num_sms) * h->d * 4;
+  return CKL_OK;
+}
+
+ckl_status ckl_norm_bwd(ckl_handle h, const void* dY, const void* q, const uint8_t* scale,
+                        const float* rstd, const void* gain, const void* d_sum, int64_t T,
+                        ckl_act8_format fmt, int accumulate, void* dX, float* dgain,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  ckl_status st = check_act8(h, T, h ? h->d : 0, fmt, q, scale);
+  if (st != CKL_OK) return st;
+  if (!gain || !dgain || (T > 0 && (!dY || !rstd || !dX))) return CKL_ERR_INVALID_ARG;
+  for (const void* p : {dY, gain, d_sum, (const void*)dX})
+    if (p && !aligned(p, 16)) return CKL_ERR_ALIGNMENT;
+  if (!aligned(dgain, 4) || (rstd && !aligned(rstd, 4))) return CKL_ERR_ALIGNMENT;
+  const int d = (int)h->d;
+  const int64_t rows = norm_part_rows(T, d, h->num_sms);
+  if (T > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)rows * d * 4))
+    return CKL_ERR_WORKSPACE;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return CKL_ERR_CUDA;
+  cudaGetLastError();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) return accumulate ? CKL_OK : cuda_status(cudaMemsetAsync(dgain, 0, (size_t)d * 4, s));
+  NormArgs a{};
+  a.x = dY; a.res = d_sum; a.gain = gain; a.T = T; a.d = d; a.fmt = fmt; a.y = dX;
+  a.q = const_cast<uint8_t*>(static_cast<const uint8_t*>(q));
+  a.e = const_cast<uint8_t*>(scale);
+  a.rstd = const_cast<float*>(rstd);
+  a.part = static_cast<float*>(workspace);
+  Launcher L{h, s};
+  const double per = elem(h) * (d_sum ? 3.0 : 2.0) + 33.0 / 32;
+  cudaError_t err = L(KID_NORM_BWD, 0, (double)T * d * per,
+                      [&] { launch_norm_bwd(a, h->dtype == CKL_BF16, h->num_sms, s); });
+  if (err == cudaSuccess)
+    err = L(KID_NORM_DGAIN, 0, (double)rows * d * 4,
+            [&] { launch_norm_dgain(a.part, rows, d, accumulate != 0, dgain, s); });
+  return cuda_status(err);
+}
+
+}  // extern "C"

@@ -1,0 +1,62 @@
+// Host-side launchers of the operators around the loss (internal; not part of the
+// C ABI). Element types: bf16 (bits) or fp32, chosen by `bf16`.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ckl {
+
+// ---- embedding (k_embed.cu)
+struct EmbedIds {
+  const int32_t* ids;   // T token ids in [0, V_total)
+  const uint8_t* mask;  // T bytes or NULL; the id of a token with mask 0 is not looked at
+  int64_t T;
+  int32_t V_total;      // ids are checked against it
+  int32_t v0, V;        // the rows held here: ids v0 .. v0 + V - 1
+  unsigned* status;
+};
+// out[t] = scale * W[ids[t] - v0] in the element type (or fp32 with out_f32); zeros for
+// masked tokens and for ids of other rows.
+void launch_embed(const EmbedIds& a, bool bf16, const void* W, int d, float scale, void* out,
+                  bool out_f32, cudaStream_t s);
+// (row, position) of every token in ascending order, as row << 32 | position; the row is V for
+// tokens that have none here. The result is in `b` if the return value is 1, else in `a`.
+int embed_sort_result(int32_t V);
+cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_b, cudaStream_t s);
+int embed_tile(int64_t T, int d, int num_sms);  // sorted tokens a thread walks
+// dW[row] (+)= scale * sum of the row's dX, in order of position. part: 2 fp32 rows for each
+// tile, the sums of rows whose tokens span tiles; launch_embed_join adds those up.
+void launch_embed_grad(const uint64_t* sorted, int64_t T, int32_t V, bool bf16, const void* dX,
+                       int d, int tile, float scale, bool accumulate, float* dW, float* part,
+                       cudaStream_t s);
+void launch_embed_join(const uint64_t* sorted, int64_t T, int32_t V, int d, int tile, float scale,
+                       bool accumulate, float* dW, const float* part, cudaStream_t s);
+
+// ---- 8-bit checkpoints and the norm (k_act8.cu)
+void launch_act8_pack(bool bf16, const void* X, int64_t T, int cols, int fmt, uint8_t* q,
+                      uint8_t* e, cudaStream_t s);
+void launch_act8_unpack(bool bf16, const uint8_t* q, const uint8_t* e, int64_t T, int cols,
+                        int fmt, void* out, cudaStream_t s);
+struct NormArgs {
+  const void* x;         // forward: input; backward: dY
+  const void* res;       // forward: residual or NULL; backward: gradient of the sum or NULL
+  const void* gain;
+  int64_t T;
+  int d;
+  float eps;
+  int fmt;
+  void* sum;             // forward: x + res (with res)
+  void* y;               // forward: output; backward: dX
+  uint8_t *q, *e;        // checkpoint (forward: NULL for none)
+  float* rstd;
+  float* part;           // backward: dgain partials, norm_part_rows x d
+};
+void launch_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t s);
+int64_t norm_part_rows(int64_t T, int d, int num_sms);
+void launch_norm_bwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s);
+// out[c] (+)= sum over rows of part[r][c], in a fixed order
+void launch_norm_dgain(const float* part, int64_t rows, int d, bool accumulate, float* out,
+                       cudaStream_t s);
+
+}  // namespace ckl

@@ -1,0 +1,174 @@
+// Device helpers of the operators around the loss (embedding, 8-bit activation
+// checkpoints, norm): eight neighbouring elements at a time, warp reductions, and
+// the 8-bit block format.
+//
+// The 8-bit format. A row's columns are cut into blocks of 32 (the last one may be
+// shorter). A block with largest magnitude A keeps one byte e + 127 and a code per
+// element, value = code * 2^e, where e >= -126 is the smallest exponent with
+// A <= M * 2^e; M is the largest code (int8: 127, e4m3: 448). Scaling by 2^-e is exact,
+// so a code is the one rounding (to nearest, ties to even) of its element: off by at
+// most half a step, 2^(e-1) < A / 127 for int8, and by at most 2^-4 of the value for
+// e4m3 above its subnormals. A power of two costs int8 up to one bit against a free
+// scale; in return every value has at most 8 significant bits and is exact in bf16, so
+// the matrix product that reads a checkpoint adds no rounding of its own. A block that
+// holds an infinity or a NaN gets the byte 255 and reads back as NaN.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include <atomic>
+
+#include "common.cuh"
+
+namespace ckl {
+
+// Allow `fn` its dynamic shared memory: once per device (a bit of `set` per ordinal), so a
+// call made during stream capture changes no attribute.
+template <typename F>
+cudaError_t smem_once(F* fn, size_t bytes, std::atomic<uint64_t>& set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
+  if (bit && (set.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+constexpr int kActInt8 = 0, kActE4m3 = 1;  // ckl_act8_format
+constexpr int kActBlock = 32;
+
+template <typename T>
+struct Raw8;  // eight elements as loaded
+template <>
+struct Raw8<uint16_t> {
+  uint4 u;
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+};
+
+__device__ __forceinline__ Raw8<uint16_t> load8(const uint16_t* p) {
+  return {*reinterpret_cast<const uint4*>(p)};
+}
+__device__ __forceinline__ Raw8<float> load8(const float* p) {
+  return {reinterpret_cast<const float4*>(p)[0], reinterpret_cast<const float4*>(p)[1]};
+}
+__device__ __forceinline__ void to_f32(const Raw8<uint16_t>& r, float (&v)[8]) {
+  v[0] = lo_bf16(r.u.x); v[1] = hi_bf16(r.u.x);
+  v[2] = lo_bf16(r.u.y); v[3] = hi_bf16(r.u.y);
+  v[4] = lo_bf16(r.u.z); v[5] = hi_bf16(r.u.z);
+  v[6] = lo_bf16(r.u.w); v[7] = hi_bf16(r.u.w);
+}
+__device__ __forceinline__ void to_f32(const Raw8<float>& r, float (&v)[8]) {
+  v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+  v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> from_f32(const float (&v)[8]);
+template <>
+__device__ __forceinline__ Raw8<uint16_t> from_f32<uint16_t>(const float (&v)[8]) {
+  return {make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                     pack_bf16x2(v[6], v[7]))};
+}
+template <>
+__device__ __forceinline__ Raw8<float> from_f32<float>(const float (&v)[8]) {
+  return {make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7])};
+}
+__device__ __forceinline__ void store8(uint16_t* p, const Raw8<uint16_t>& r) {
+  *reinterpret_cast<uint4*>(p) = r.u;
+}
+__device__ __forceinline__ void store8(float* p, const Raw8<float>& r) {
+  reinterpret_cast<float4*>(p)[0] = r.a;
+  reinterpret_cast<float4*>(p)[1] = r.b;
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> zero8() {
+  const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  return from_f32<T>(z);
+}
+
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Bits of the largest magnitude among v (a NaN's bits are above every other's).
+__device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+// The same over the four lanes of a block (the whole warp calls it).
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+// Scale byte of a block: 127 = 1.984375 * 2^6 and 448 = 1.75 * 2^8, so the smallest
+// exponent follows from the magnitude's own exponent and fraction bits.
+__device__ __forceinline__ uint32_t act8_scale_byte(uint32_t amax, int fmt) {
+  const int ex = (int)(amax >> 23);
+  if (ex == 255) return 255u;
+  const uint32_t frac = amax & 0x7FFFFFu;
+  const int b = fmt == kActInt8 ? ex - 6 + (frac > 0x7E0000u) : ex - 8 + (frac > 0x600000u);
+  return (uint32_t)max(b, 1);
+}
+// Codes of eight elements under the block's scale byte.
+__device__ __forceinline__ uint2 act8_encode(const float (&v)[8], uint32_t byte, int fmt) {
+  if (byte == 255u) return make_uint2(0u, 0u);
+  const float inv = __uint_as_float((254u - byte) << 23);  // 2^-e
+  float u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = v[i] * inv;
+  if (byte >= 247u) {
+    // the largest magnitudes of fp32 and bf16 would round up to 2^128: the code below it
+    const float lim = fmt == kActE4m3 ? 240.f : byte >= 249u ? 63.f : 127.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = fminf(fmaxf(u[i], -lim), lim);
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (fmt == kActInt8) {
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = (uint32_t)__float2int_rn(u[4 * j + i]) & 0xFFu;
+      w[j] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+    } else {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(u[4 * j], u[4 * j + 1]),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(u[4 * j + 2], u[4 * j + 3]),
+                                                   __NV_SATFINITE, __NV_E4M3);
+      w[j] = lo | hi << 16;
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ float act8_scale(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7FC00000u : byte << 23);
+}
+__device__ __forceinline__ void act8_decode(uint2 q, float scale, int fmt, float (&v)[8]) {
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (fmt == kActInt8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * j + i] = (float)(int8_t)(w[j] >> (8 * i)) * scale;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j] >> (16 * i)),
+                                                   __NV_E4M3));
+        const float2 f = __half22float2(h);
+        v[4 * j + 2 * i] = f.x * scale;
+        v[4 * j + 2 * i + 1] = f.y * scale;
+      }
+    }
+  }
+}
+
+}  // namespace ckl

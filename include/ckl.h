@@ -275,6 +275,89 @@ ckl_status ckl_topk_cache_vocab_parallel(ckl_handle h, const ckl_vocab_group* gr
                                          int32_t* topk_idx, float* topk_logit, void* workspace,
                                          size_t workspace_bytes, void* stream, int wait);
 
+/* ---- Operators around the loss ----
+ *
+ * The two ends of the model that the loss trains: the embedding, whose weight W is the LM
+ * head's own where the two are tied, and the norm before the head, whose input is kept for
+ * the backward pass in 8 bits. They take a handle for its device, dtype and hidden size d
+ * (the embedding also for V, the rows of W held; K and max_chunk do not matter to them).
+ * The conventions at the top hold. T <= 2^31 - 1. All results are deterministic: no sum's
+ * order depends on timing. All calls can be captured in a CUDA graph once each has run
+ * (wait = 0 where there is that argument). */
+
+/* out[t] = scale * W[ids[t] - v0], rounded once to the handle's dtype (T x d).
+ * mask may be NULL; a token with mask 0 gets a row of zeros and its id is not looked at.
+ * Ids are in [0, V_total); the handle's V rows of W are ids v0 .. v0 + V - 1 (v0 = 0 and
+ * V_total = V where all rows are here), and an id of another rank's row gives zeros. An id
+ * outside [0, V_total) gives zeros and sets the status CKL_ERR_INDEX_RANGE.
+ * wait != 0: wait for the stream and return the device-detected status. */
+ckl_status ckl_embed(ckl_handle h, const int32_t* ids, const uint8_t* mask, const void* W,
+                     int64_t T, int64_t V_total, int64_t v0, float scale, void* out, void* stream,
+                     int wait);
+
+/* As ckl_embed with W split by vocabulary rows over a group (ckl_vocab_group above; bf16
+ * handles, all_gather is not used and may be NULL): each rank looks up its own rows in fp32
+ * and one all-reduce of T x d floats adds the ranks' rows (none for T = 0), so out is the
+ * same on every rank and the same as ckl_embed with all of W. Workspace:
+ * ckl_embed_vp_workspace_bytes. Errors as in ckl_fwd_bwd_vocab_parallel. */
+ckl_status ckl_embed_vp_workspace_bytes(ckl_handle h, int64_t T, size_t* bytes);
+ckl_status ckl_embed_vocab_parallel(ckl_handle h, const ckl_vocab_group* group, const int32_t* ids,
+                                    const uint8_t* mask, const void* W_shard, int64_t T,
+                                    float scale, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream, int wait);
+
+/* Gradient of ckl_embed with respect to W:
+ *     dW[v] (+)= scale * sum over the unmasked t with ids[t] = v0 + v of dX[t]
+ * dX: T x d, the handle's dtype. dW: V x d fp32. accumulate != 0 adds to dW, for example to
+ * the dW that ckl_fwd_bwd wrote for a tied head, and leaves the rows of ids that do not
+ * occur as they are; otherwise dW is overwritten (zeros where no token falls). A row's sum is
+ * formed in fp32 in order of position and multiplied by scale once. Tokens with mask 0, ids of
+ * other ranks' rows and ids outside [0, V_total) (status CKL_ERR_INDEX_RANGE) add nothing.
+ * Workspace: ckl_embed_grad_workspace_bytes, O(T): 16 T bytes and at most 2 T d. */
+ckl_status ckl_embed_grad_workspace_bytes(ckl_handle h, int64_t T, size_t* bytes);
+ckl_status ckl_embed_grad(ckl_handle h, const int32_t* ids, const uint8_t* mask, const void* dX,
+                          int64_t T, int64_t V_total, int64_t v0, float scale, int accumulate,
+                          float* dW, void* workspace, size_t workspace_bytes, void* stream,
+                          int wait);
+
+/* 8-bit activation checkpoints: T rows of `cols` columns (cols % 8 == 0, cols <= 2^20), kept
+ * as q (T x cols bytes, 16-byte aligned) and scale (T x ceil(cols / 32) bytes). Each block of
+ * 32 columns of a row (the last may be shorter) has one scale 2^e, kept as the byte e + 127;
+ * element = code * 2^e with the code a two's-complement byte, |code| <= 127
+ * (CKL_ACT8_INT8), or an e4m3 value, at most 448 (CKL_ACT8_E4M3). e >= -126 is the smallest
+ * exponent that holds the block's largest magnitude, and a code is its element / 2^e rounded
+ * to nearest, ties to even (down where up would read back as 2^128). A block with an infinity or a NaN gets the byte 255, which reads
+ * back as NaN. Values read back are exact in fp32 and, above 2^-126, in bf16. */
+typedef enum { CKL_ACT8_INT8 = 0, CKL_ACT8_E4M3 = 1 } ckl_act8_format;
+ckl_status ckl_act8_pack(ckl_handle h, const void* X, int64_t T, int64_t cols, ckl_act8_format fmt,
+                         void* q, uint8_t* scale, void* stream);
+ckl_status ckl_act8_unpack(ckl_handle h, const void* q, const uint8_t* scale, int64_t T,
+                           int64_t cols, ckl_act8_format fmt, void* out, void* stream);
+
+/* RMS norm with the residual addition in the same pass. With s = X + residual rounded to
+ * the handle's dtype (s = X where residual is NULL):
+ *     rstd_t = 1 / sqrt(mean(s_t^2) + eps),   Y_t = s_t rstd_t gain   (rounded once)
+ * X, residual, sum, Y: T x d; gain: d; all in the handle's dtype. eps > 0. With a residual,
+ * s is written to sum (which may be X's or residual's buffer; Y may be the other's).
+ * q and scale (both or neither) receive the checkpoint of s in the format fmt, and rstd (T
+ * floats, needed with them) each row's factor: together all that ckl_norm_bwd reads. */
+ckl_status ckl_norm(ckl_handle h, const void* X, const void* residual, const void* gain, int64_t T,
+                    float eps, ckl_act8_format fmt, void* sum, void* Y, void* q, uint8_t* scale,
+                    float* rstd, void* stream);
+
+/* Backward of ckl_norm from its checkpoint. With s' the checkpoint's values, h = s' rstd and
+ * a = dY gain:
+ *     dX = rstd (a - h mean(a h)) + d_sum    (rounded once; the gradient of X and of residual)
+ *     dgain (+)= sum_t dY_t h_t              (d floats)
+ * d_sum (T x d or NULL): the gradient that reaches s other than through Y. dX may be dY's or
+ * d_sum's buffer. accumulate != 0 adds to dgain; otherwise it is overwritten. Workspace:
+ * ckl_norm_bwd_workspace_bytes (bounded: a few rows of d floats per SM). */
+ckl_status ckl_norm_bwd_workspace_bytes(ckl_handle h, int64_t T, size_t* bytes);
+ckl_status ckl_norm_bwd(ckl_handle h, const void* dY, const void* q, const uint8_t* scale,
+                        const float* rstd, const void* gain, const void* d_sum, int64_t T,
+                        ckl_act8_format fmt, int accumulate, void* dX, float* dgain,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* Wait for `stream` and return the device-detected status of the calls enqueued
  * on it since the last synchronising call (clears it). */
 ckl_status ckl_sync_status(ckl_handle h, void* stream);

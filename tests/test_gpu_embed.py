@@ -1,0 +1,272 @@
+"""Embedding lookup and its gradient by sorted tokens, against the fp64 oracle.
+
+Bounds, with u = 2^-24 (half a step of fp32) and n the tokens of a row: a looked-up element is
+one fp32 product and one rounding to its type (half a step, eps / 2 of the value). A gradient
+element is n - 1 additions in some order, one product with the scale and one addition to what
+was there, so it is off by at most (n + 2) u times the sum of the magnitudes that enter it
+(1.01: the higher orders).
+"""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from chunked_kl_loss_logits_b200 import ckl
+from oracle import ops_oracle as O
+from tests._helpers import f64
+from tests.test_gpu_vocab_parallel import ThreadGroup
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def case(T, d, V, dt, seed=0, masked=False, hot=0.0):
+    g = torch.Generator().manual_seed(seed + T + d + V)
+    ids = torch.randint(0, V, (T,), generator=g, dtype=torch.int32)
+    ids[torch.rand(T, generator=g) < hot] = V // 2  # a frequent token
+    mask = (torch.rand(T, generator=g) < 0.8).to(torch.uint8) if masked else None
+    W = torch.randn(V, d, generator=g).to(DT[dt])
+    dX = torch.randn(T, d, generator=g).to(DT[dt])
+    return [None if t is None else t.cuda() for t in (ids, mask, W, dX)]
+
+
+def check_grad(dW, ids, dX, V, mask, scale, base=None, v0=0):
+    keep = None if mask is None else mask.cpu().numpy()
+    want, mag = O.embed_grad(ids.cpu().numpy(), f64(dX), V, keep, scale, v0,
+                             None if base is None else f64(base))
+    local = ids.cpu().numpy().astype(np.int64) - v0
+    sel = (local >= 0) & (local < V) & (True if keep is None else keep != 0)
+    n = np.bincount(local[sel], minlength=V)[:, None]
+    err = np.abs(f64(dW) - want)
+    assert np.all(err <= 1.01 * (n + 2) * U * mag), float((err - 1.01 * (n + 2) * U * mag).max())
+    if base is not None:  # rows without a token are left as they were
+        assert torch.equal(dW[torch.from_numpy(n[:, 0] == 0).cuda()],
+                           base[torch.from_numpy(n[:, 0] == 0).cuda()])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,V", [(1, 8, 1), (3, 64, 5), (65, 136, 777), (257, 2880, 3001),
+                                   (300, 1032, 512)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_embed(T, d, V, dt, masked):
+    ids, mask, W, _ = case(T, d, V, dt, masked=masked)
+    h = ckl.operator_handle(W, V=V)
+    out = h.embed(ids, W, mask=mask, scale=3.7)
+    want = O.embed(ids.cpu().numpy(), f64(W), None if mask is None else mask.cpu().numpy(),
+                   float(np.float32(3.7)))
+    half = torch.finfo(DT[dt]).eps / 2
+    assert np.all(np.abs(f64(out) - want) <= (half + 1.01 * U) * np.abs(want))
+    out2 = h.embed(ids.view(1, T), W, mask=mask, scale=3.7)
+    assert out2.shape == (1, T, d) and torch.equal(out2[0], out)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,V,hot", [
+    (1, 8, 1, 0), (2, 64, 1, 0), (33, 136, 777, 0), (700, 64, 5, 0.3),
+    (1025, 264, 511, 0.1),     # two CTAs sort; 9-bit keys
+    (5000, 72, 512, 0.5),      # 10-bit keys in two digits; a row over many tiles
+    (4097, 128, 70000, 0),     # nearly all rows distinct
+])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad(T, d, V, hot, dt, accumulate):
+    ids, mask, W, dX = case(T, d, V, dt, masked=T % 2 == 1, hot=hot)
+    if mask is not None and T > 4:
+        dX[mask == 0] = float("nan")  # what a masked place holds does not matter
+    h = ckl.operator_handle(W, V=V)
+    base = torch.randn(V, d, device="cuda")
+    runs = []
+    for _ in range(2):
+        dW = base.clone() if accumulate else torch.full((V, d), float("nan"), device="cuda")
+        got = h.embed_grad(ids, dX, mask=mask, scale=0.37, dW=dW, accumulate=accumulate)
+        assert got is dW
+        runs.append(dW)
+    assert torch.equal(*runs)
+    clean = torch.nan_to_num(dX.float()).to(dX.dtype)
+    check_grad(runs[0], ids, clean, V, mask, float(np.float32(0.37)), base if accumulate else None)
+
+
+def test_embed_grad_one_row_takes_every_token():
+    for T in (31, 32, 33, 64, 65, 4096, 40000):
+        ids = torch.full((T,), 6, dtype=torch.int32, device="cuda")
+        dX = torch.randn(T, 8, device="cuda")
+        h = ckl.operator_handle(dX, V=9)
+        check_grad(h.embed_grad(ids, dX), ids, dX, 9, None, 1.0)
+
+
+def test_embed_grad_many_tokens_three_digits():
+    """A long sequence (every CTA of the sort walks its range several times) and a vocabulary
+    of 19 bits; integers, so that every order of the sums is exact."""
+    T, d, V = 150001, 16, 300000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    ids = (torch.rand(T, generator=g, device="cuda") ** 6 * V).to(torch.int32)
+    dX = torch.randint(-4, 5, (T, d), generator=g, device="cuda").to(torch.bfloat16)
+    h = ckl.operator_handle(dX, V=V)
+    want = torch.zeros(V, d, dtype=torch.float64, device="cuda").index_add_(0, ids.long(), dX.double())
+    assert torch.equal(h.embed_grad(ids, dX).double(), want)
+
+
+def test_masks_and_lengths_that_leave_nothing():
+    ids, _, W, dX = case(40, 64, 30, "bf16")
+    h = ckl.operator_handle(W, V=30)
+    none = torch.zeros(40, dtype=torch.uint8, device="cuda")
+    wild = torch.full_like(ids, -1)  # the ids of masked tokens are not looked at
+    assert torch.all(h.embed(wild, W, mask=none) == 0)
+    assert torch.all(h.embed_grad(wild, dX, mask=none) == 0)
+    base = torch.randn(30, 64, device="cuda")
+    assert torch.equal(h.embed_grad(wild, dX, mask=none, dW=base.clone(), accumulate=True), base)
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert h.embed(e, W).shape == (0, 64)
+    dX0 = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
+    assert torch.all(h.embed_grad(e, dX0, dW=torch.ones(30, 64, device="cuda")) == 0)
+    assert torch.equal(h.embed_grad(e, dX0, dW=base.clone(), accumulate=True), base)
+
+
+@pytest.mark.parametrize("bad", [-1, 30, 2 ** 31 - 1])
+def test_an_id_out_of_range_is_reported_and_adds_nothing(bad):
+    ids, _, W, dX = case(40, 64, 30, "bf16")
+    ids[7] = bad
+    h = ckl.operator_handle(W, V=30)
+    out = torch.empty(40, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ckl.CKLError) as e:
+        h.embed(ids, W, out=out)
+    assert e.value.code == 4 and torch.all(out[7] == 0)
+    dW = torch.empty(30, 64, device="cuda")
+    with pytest.raises(ckl.CKLError) as e:
+        h.embed_grad(ids, dX, dW=dW)
+    assert e.value.code == 4
+    keep = torch.ones(40, dtype=torch.uint8, device="cuda")
+    keep[7] = 0
+    assert torch.equal(dW, h.embed_grad(ids, dX, mask=keep))  # the status was cleared
+
+
+def test_shards_of_the_vocabulary():
+    ids, mask, W, dX = case(300, 64, 100, "bf16", masked=True)
+    whole = ckl.operator_handle(W, V=100)
+    out, dW = whole.embed(ids, W, mask=mask), whole.embed_grad(ids, dX, mask=mask)
+    total = torch.zeros_like(out)
+    for v0, n in ((0, 37), (37, 63)):
+        h = ckl.operator_handle(W, V=n)
+        total += h.embed(ids, W[v0:v0 + n], mask=mask, V_total=100, v0=v0)
+        assert torch.equal(h.embed_grad(ids, dX, mask=mask, V_total=100, v0=v0), dW[v0:v0 + n])
+    assert torch.equal(total, out)
+
+
+def test_embed_vocab_parallel():
+    ids, mask, W, _ = case(130, 128, 700, "bf16", masked=True)
+    want = ckl.operator_handle(W, V=700).embed(ids, W, mask=mask, scale=2.5)
+    torch.cuda.synchronize()
+    shards, tg, got, errs = ckl.vocab_shards(700, 2), ThreadGroup(2), [None, None], []
+
+    def rank(r):
+        try:
+            v0, n = shards[r]
+            h = ckl.ChunkedKL(n, 128, 4, max_chunk=64)
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                got[r] = h.embed_vocab_parallel(tg.member(r, 700, v0), ids, W[v0:v0 + n], mask,
+                                                scale=2.5).cpu()
+            h.close()
+        except Exception as e:
+            errs.append(e)
+            tg.barrier.abort()
+
+    th = [threading.Thread(target=rank, args=(r,)) for r in range(2)]
+    [t.start() for t in th]
+    [t.join(120) for t in th]
+    assert not errs, errs
+    assert torch.equal(got[0], want.cpu()) and torch.equal(got[1], want.cpu())
+    assert tg.calls[0] == [("reduce", 130 * 128)] and tg.calls[0] == tg.calls[1]
+
+
+def test_long_sequences_pass_32_bit_offsets():
+    T, d, V = 760000, 2880, 64  # 2.19e9 elements
+    W = torch.randn(V, d, device="cuda").to(torch.bfloat16)
+    ids = torch.randint(0, V - 1, (T,), device="cuda", dtype=torch.int32)
+    ids[-5:] = V - 1
+    h = ckl.operator_handle(W, V=V)
+    out = h.embed(ids, W)
+    assert torch.equal(out[-9:], W[ids[-9:].long()])
+    out.zero_()
+    out[-5:] = 1.0  # as dX: the last row's gradient comes from the far end alone
+    dW = h.embed_grad(ids, out)
+    assert torch.all(dW[:-1] == 0) and torch.all(dW[-1] == 5.0)
+
+
+def test_calls_captured_in_a_graph_and_on_a_stream():
+    ids, mask, W, dX = case(3000, 264, 900, "bf16", masked=True, hot=0.2)
+    h = ckl.operator_handle(W, V=900)
+    out, dW = torch.empty_like(dX), torch.empty(900, 264, device="cuda")
+    ws = h._workspace("ckl_embed_grad_workspace_bytes", 3000)
+    call = lambda: (h.embed(ids, W, mask=mask, out=out, sync=False),
+                    h.embed_grad(ids, dX, mask=mask, dW=dW, workspace=ws, sync=False))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for seed in (1, 2):
+        ids2, _, _, dX2 = case(3000, 264, 900, "bf16", seed=seed, hot=0.4 * seed)
+        ids.copy_(ids2)
+        dX.copy_(dX2)
+        out.fill_(7)
+        dW.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, h.embed(ids, W, mask=mask))
+        assert torch.equal(dW, h.embed_grad(ids, dX, mask=mask))
+
+
+def test_autograd_embedding():
+    ids, mask, W, dX = case(500, 64, 90, "f32", masked=True)
+    W.requires_grad_()
+    out = ckl.embedding(ids.view(5, 100), W, mask=mask, scale=2.0)
+    assert out.shape == (5, 100, 64)
+    out.backward(dX.view(5, 100, 64))
+    check_grad(W.grad, ids, dX, 90, mask, 2.0)
+    W.grad = None
+    ckl.embedding(ids, W).sum().backward()  # an expanded gradient
+    n = torch.bincount(ids.long(), minlength=90).float()[:, None].expand(90, 64)
+    assert torch.equal(W.grad, n)
+    ids[3] = 90
+    with pytest.raises(ckl.CKLError):
+        ckl.embedding(ids, W).sum().backward()
+
+
+def test_refusals():
+    ids, mask, W, dX = case(40, 64, 30, "bf16")
+    h = ckl.operator_handle(W, V=30)
+    with pytest.raises(TypeError):
+        h.embed(ids.long(), W)
+    with pytest.raises(TypeError):
+        h.embed(ids, W.float())
+    with pytest.raises(ValueError):
+        h.embed(ids, W[:29])
+    with pytest.raises(TypeError):
+        h.embed(ids, W, mask=torch.ones(39, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        h.embed(ids[::2], W)
+    with pytest.raises(ValueError):
+        h.embed(ids.cpu(), W)
+    with pytest.raises(ValueError):
+        h.embed_grad(ids, dX, accumulate=True)
+    with pytest.raises(ValueError):
+        h.embed_grad(ids, dX[:39])
+    with pytest.raises(TypeError):
+        h.embed_grad(ids, dX, dW=torch.empty(30, 64, device="cuda", dtype=torch.bfloat16))
+    for kw in ({"scale": float("nan")}, {"scale": float("inf")}, {"v0": -1}, {"v0": 1},
+               {"V_total": 29}):
+        with pytest.raises(ckl.CKLError) as e:
+            h.embed(ids, W, **kw)
+        assert e.value.code == 1
+    with pytest.raises(ckl.CKLError) as e:
+        h.embed_grad(ids, dX, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == 3
+    shifted = torch.empty(30 * 64 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(30, 64)
+    with pytest.raises(ckl.CKLError) as e:
+        h.embed(ids, shifted)
+    assert e.value.code == 7
