@@ -103,6 +103,10 @@ def lib() -> ctypes.CDLL:
                             _SZ, _P, ctypes.c_int], ctypes.c_int),
         "ckl_act8_pack": ([_P, _P, _I64, _I64, ctypes.c_int, _P, _P, _P], ctypes.c_int),
         "ckl_act8_unpack": ([_P, _P, _P, _I64, _I64, ctypes.c_int, _P, _P], ctypes.c_int),
+        "ckl_act8_weight_grad_workspace_bytes": ([_P, _I64, _I64, _I64, ctypes.POINTER(_SZ)],
+                                                 ctypes.c_int),
+        "ckl_act8_weight_grad": ([_P, _P, _I64, _I64, _P, _P, _I64, ctypes.c_int, ctypes.c_int, _P,
+                                  _P, _SZ, _P, ctypes.c_int], ctypes.c_int),
         "ckl_norm": ([_P, _P, _P, _P, _I64, ctypes.c_float, ctypes.c_int, _P, _P, _P, _P, _P, _P],
                      ctypes.c_int),
         "ckl_norm_bwd_workspace_bytes": ([_P, _I64, ctypes.POINTER(_SZ)], ctypes.c_int),
@@ -293,12 +297,12 @@ class ChunkedKL:
         _check(lib().ckl_profile_enable(self._h, int(on), max_launches), "ckl_profile_enable")
 
     def profile_collect(self) -> list:
-        arr = (KernelStat * 32)()
+        arr = (KernelStat * 64)()
         n = ctypes.c_int()
-        _check(lib().ckl_profile_collect(self._h, arr, 32, ctypes.byref(n)), "ckl_profile_collect")
+        _check(lib().ckl_profile_collect(self._h, arr, 64, ctypes.byref(n)), "ckl_profile_collect")
         return [{"name": arr[i].name.decode(), "launches": arr[i].launches,
                  "total_ms": arr[i].total_ms, "flops": arr[i].flops, "bytes": arr[i].bytes}
-                for i in range(min(n.value, 32))]
+                for i in range(min(n.value, 64))]
 
     def selftest_wait_bound(self, stream=None):
         """(status code, SM cycles waited) of the bounded-wait self-test; 6 (timeout) is a pass."""
@@ -613,6 +617,28 @@ class ChunkedKL:
         _check(lib().ckl_act8_unpack(self._h, _ptr(ckpt.q), _ptr(ckpt.scale), *ckpt.q.shape, f,
                                      _ptr(out), self._stream(stream)), "ckl_act8_unpack")
         return out
+
+    def act8_weight_grad(self, dY, ckpt: Act8, dW=None, accumulate: bool = False, workspace=None,
+                         sync: bool = True, stream=None):
+        """dW = dY^T X' (n x cols, float32) of a linear layer Y = X W^T with X kept as the
+        checkpoint; dY is T x n. dW is added to with accumulate=True."""
+        f = self._act8(ckpt)
+        T, cols = ckpt.q.shape
+        if dY.dim() != 2 or dY.shape[0] != T:
+            raise ValueError("dY must be T x n, a row for each row of the checkpoint")
+        self._rows("dY", dY)
+        n = dY.shape[1]
+        if dW is None:
+            if accumulate:
+                raise ValueError("accumulate needs dW")
+            dW = torch.empty((n, cols), dtype=torch.float32, device=self.device)
+        self._f32("dW", dW, (n, cols))
+        ws = workspace if workspace is not None else \
+            self._workspace("ckl_act8_weight_grad_workspace_bytes", T, n, cols)
+        _check(lib().ckl_act8_weight_grad(self._h, _ptr(dY), T, n, _ptr(ckpt.q), _ptr(ckpt.scale),
+                                          cols, f, int(accumulate), _ptr(dW), _ptr(ws), ws.numel(),
+                                          self._stream(stream), int(sync)), "ckl_act8_weight_grad")
+        return dW
 
     def norm(self, x, gain, residual=None, eps: float = 1e-5, checkpoint: str | None = "int8",
              out=None, stream=None):

@@ -1,7 +1,7 @@
 // C ABI of the operators around the loss: the embedding (the other end of a tied LM
-// head), 8-bit activation checkpoints, and the RMS norm that keeps its input in one.
-// Argument checks, workspace plans and launches; the kernels are in k_embed.cu and
-// k_act8.cu.
+// head), 8-bit activation checkpoints with the weight gradient that reads one, and the
+// RMS norm that keeps its input in one. Argument checks, workspace plans and launches;
+// the kernels are in k_embed.cu, k_act8.cu and k_wgrad.cu.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -66,9 +66,98 @@ ckl_status check_act8(const ckl_ctx* h, int64_t T, int64_t cols, int fmt, const 
   return CKL_OK;
 }
 
+struct WgradPlan {
+  int64_t parts = 0, kb_part = 0, n_kb = 0, kb_split = 0;
+  int n_split = 1;
+  size_t off_parts = 0, off_sum = 0, total = 0;
+};
+
+WgradPlan wgrad_plan(const ckl_ctx* h, int64_t T, int64_t n, int64_t cols) {
+  WgradPlan p;
+  p.parts = h->dtype == CKL_BF16 ? 1 : 3;
+  p.kb_part = (T + 63) / 64;
+  p.n_kb = p.parts * p.kb_part;
+  p.n_split = p.n_kb ? wgrad_split(n, cols, p.n_kb, h->num_sms) : 1;
+  p.kb_split = (p.n_kb + p.n_split - 1) / p.n_split;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
+  if (p.parts > 1) p.off_parts = take((size_t)T * n * 2 * p.parts);
+  if (p.n_split > 1) p.off_sum = take((size_t)p.n_split * n * cols * 4);
+  p.total = o;
+  return p;
+}
+
+ckl_status check_wgrad(const ckl_ctx* h, int64_t T, int64_t n, int64_t cols) {
+  if (!h || T < 0 || n < 1 || cols < 1) return CKL_ERR_INVALID_ARG;
+  if (n % 8 != 0 || cols % 8 != 0 || n > (1 << 20) || cols > (1 << 20) ||
+      T > (int64_t)INT32_MAX / 4)
+    return CKL_ERR_UNSUPPORTED;
+  return CKL_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+ckl_status ckl_act8_weight_grad_workspace_bytes(ckl_handle h, int64_t T, int64_t n, int64_t cols,
+                                                size_t* bytes) {
+  const ckl_status st = check_wgrad(h, T, n, cols);
+  if (st != CKL_OK || !bytes) return st != CKL_OK ? st : CKL_ERR_INVALID_ARG;
+  *bytes = wgrad_plan(h, T, n, cols).total;
+  return CKL_OK;
+}
+
+ckl_status ckl_act8_weight_grad(ckl_handle h, const void* dY, int64_t T, int64_t n, const void* q,
+                                const uint8_t* scale, int64_t cols, ckl_act8_format fmt,
+                                int accumulate, float* dW, void* workspace, size_t workspace_bytes,
+                                void* stream, int wait) {
+  ckl_status st = check_wgrad(h, T, n, cols);
+  if (st == CKL_OK) st = check_act8(h, T, cols, fmt, q, scale);
+  if (st != CKL_OK) return st;
+  if (!dW || (T > 0 && !dY)) return CKL_ERR_INVALID_ARG;
+  if (!aligned(dW, 16) || (dY && !aligned(dY, 16))) return CKL_ERR_ALIGNMENT;
+  const WgradPlan P = wgrad_plan(h, T, n, cols);
+  if (P.total && (!workspace || !aligned(workspace, 256) || workspace_bytes < P.total))
+    return CKL_ERR_WORKSPACE;
+  DeviceGuard guard(h->device);
+  if (!guard.ok) return CKL_ERR_CUDA;
+  cudaGetLastError();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t err = cudaSuccess;
+  auto chk = [&](cudaError_t e) { if (e != cudaSuccess && err == cudaSuccess) err = e; };
+  if (T == 0) {
+    if (!accumulate) chk(cudaMemsetAsync(dW, 0, (size_t)n * cols * 4, s));
+  } else {
+    unsigned char* base = static_cast<unsigned char*>(workspace);
+    Launcher L{h, s};
+    const void* a = dY;
+    if (P.parts > 1) {
+      uint16_t* parts = reinterpret_cast<uint16_t*>(base + P.off_parts);
+      chk(L(KID_WGRAD_PARTS, 0, (double)T * n * 10,
+            [&] { launch_split3(static_cast<const float*>(dY), T * n, parts, s); }));
+      a = parts;
+    }
+    CUtensorMap map;
+    if (!make_map_planes(h, &map, a, n, T, P.parts)) return CKL_ERR_CUDA;
+    WgradArgs p{};
+    p.q = static_cast<const uint8_t*>(q);
+    p.e = scale;
+    p.T = T;
+    p.n = (int)n; p.cols = (int)cols; p.nb = (int)((cols + 31) / 32);
+    p.kb_part = (int)P.kb_part; p.n_kb = (int)P.n_kb;
+    p.n_split = P.n_split; p.kb_split = (int)P.kb_split;
+    p.add = P.n_split == 1 && accumulate;
+    p.out = P.n_split > 1 ? reinterpret_cast<float*>(base + P.off_sum) : dW;
+    p.status = h->d_status;
+    chk(L(KID_WGRAD, 2.0 * T * n * cols, 0,
+          [&] { chk(launch_wgrad(map, p, fmt, h->num_sms, s)); }));
+    if (P.n_split > 1)
+      chk(L(KID_WGRAD_SUM, 0, 4.0 * n * cols * (P.n_split + 1),
+            [&] { launch_wgrad_sum(p.out, P.n_split, n * cols, accumulate != 0, dW, s); }));
+  }
+  if ((st = cuda_status(err)) != CKL_OK) return st;
+  return wait ? sync_and_read(h, s, nullptr, nullptr) : CKL_OK;
+}
 
 ckl_status ckl_embed(ckl_handle h, const int32_t* ids, const uint8_t* mask, const void* W,
                      int64_t T, int64_t V_total, int64_t v0, float scale, void* out, void* stream,

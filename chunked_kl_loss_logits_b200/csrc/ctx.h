@@ -28,7 +28,8 @@ enum KernelId {
   KID_DW, KID_LOSS, KID_TKMAX, KID_TKTHRESH, KID_TKEMIT, KID_TKSELECT, KID_VP_MERGE,
   KID_DH_F32, KID_TO_BF16, KID_VP_GATHER, KID_VP_REDUCE,
   KID_EMBED, KID_EMBED_SORT, KID_EMBED_GRAD, KID_EMBED_JOIN, KID_ACT8_PACK, KID_ACT8_UNPACK,
-  KID_NORM_FWD, KID_NORM_BWD, KID_NORM_DGAIN, KID_WGRAD, KID_WGRAD_SUM, KID_COUNT
+  KID_NORM_FWD, KID_NORM_BWD, KID_NORM_DGAIN, KID_WGRAD_PARTS, KID_WGRAD, KID_WGRAD_SUM,
+  KID_COUNT
 };
 // bf16 backward: a profiled "dh_gemm" range also holds the next chunk's teacher
 // kernel, and a "dw_gemm" range the chunk's dH split reduction, both launched
@@ -40,7 +41,8 @@ inline const char* const kKernelNames[KID_COUNT] = {"mask_count", "teacher_topk"
                                        "vp_merge", "dh_reduce_f32", "dh_to_bf16",
                                        "vp_all_gather", "vp_all_reduce", "embed", "embed_sort",
                                        "embed_grad", "embed_join", "act8_pack", "act8_unpack",
-                                       "norm_fwd", "norm_bwd", "norm_dgain", "act8_weight_grad",
+                                       "norm_fwd", "norm_bwd", "norm_dgain", "weight_grad_parts",
+                                       "act8_weight_grad",
                                        "weight_grad_sum"};
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -101,6 +103,20 @@ inline bool make_map(const ckl_ctx* h, CUtensorMap* m, const void* base, uint64_
                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// 3-D bf16 tensor map of `outer` planes of rows x inner, dense; boxes of 64 x 64 x 1, 128-byte
+// swizzle, zero fill outside.
+inline bool make_map_planes(const ckl_ctx* h, CUtensorMap* m, const void* base, uint64_t inner,
+                            uint64_t rows, uint64_t outer) {
+  const cuuint64_t dims[3] = {inner, rows, outer};
+  const cuuint64_t strides[2] = {inner * 2, inner * rows * 2};
+  const cuuint32_t box[3] = {64, 64, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Every launch (and every caller-supplied collective) is wrapped in an NVTX range

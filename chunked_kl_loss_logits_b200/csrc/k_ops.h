@@ -2,6 +2,7 @@
 // C ABI). Element types: bf16 (bits) or fp32, chosen by `bf16`.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -58,5 +59,25 @@ void launch_norm_bwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s);
 // out[c] (+)= sum over rows of part[r][c], in a fixed order
 void launch_norm_dgain(const float* part, int64_t rows, int d, bool accumulate, float* out,
                        cudaStream_t s);
+
+// ---- weight gradient from a checkpoint (k_wgrad.cu)
+struct WgradArgs {
+  const uint8_t *q, *e;
+  int64_t T;
+  int n, cols, nb;  // dY columns, X' columns, blocks of a row of X'
+  int kb_part;      // 64-token steps of one part of dY
+  int n_kb;         // steps in all (parts x kb_part)
+  int n_split, kb_split;
+  int add;          // add to out (n_split == 1 only)
+  float* out;       // n x cols, or n_split partial results of that size
+  unsigned* status;
+};
+int wgrad_split(int64_t n, int64_t cols, int64_t n_kb, int num_sms);
+// a: the bf16 parts of dY as a (n, T, parts) tensor, boxes of 64 x 64 x 1
+cudaError_t launch_wgrad(const CUtensorMap& a, const WgradArgs& p, int fmt, int num_sms,
+                         cudaStream_t s);
+void launch_split3(const float* x, int64_t n, uint16_t* out, cudaStream_t s);
+void launch_wgrad_sum(const float* part, int n_split, int64_t n, bool add, float* out,
+                      cudaStream_t s);
 
 }  // namespace ckl

@@ -334,6 +334,21 @@ ckl_status ckl_act8_pack(ckl_handle h, const void* X, int64_t T, int64_t cols, c
 ckl_status ckl_act8_unpack(ckl_handle h, const void* q, const uint8_t* scale, int64_t T,
                            int64_t cols, ckl_act8_format fmt, void* out, void* stream);
 
+/* Weight gradient of a linear layer Y = X W^T whose input X was kept as a checkpoint:
+ *     dW[i][c] (+)= sum_t dY[t][i] X'[t][c]
+ * with X' the checkpoint's values (T x cols) and dY T x n (n % 8 == 0, the handle's dtype).
+ * dW: n x cols fp32, added to with accumulate != 0 and overwritten otherwise. Products are
+ * exact and summed in fp32 (fp32 dY as three bf16 parts that add up to it). T < 2^29. Runs on
+ * the tensor cores of sm_100a. Workspace: ckl_act8_weight_grad_workspace_bytes (6 T n bytes
+ * for fp32, and a partial dW for each range of tokens where n x cols alone does not fill the
+ * GPU); it may be NULL where that is 0. */
+ckl_status ckl_act8_weight_grad_workspace_bytes(ckl_handle h, int64_t T, int64_t n, int64_t cols,
+                                                size_t* bytes);
+ckl_status ckl_act8_weight_grad(ckl_handle h, const void* dY, int64_t T, int64_t n, const void* q,
+                                const uint8_t* scale, int64_t cols, ckl_act8_format fmt,
+                                int accumulate, float* dW, void* workspace, size_t workspace_bytes,
+                                void* stream, int wait);
+
 /* RMS norm with the residual addition in the same pass. With s = X + residual rounded to
  * the handle's dtype (s = X where residual is NULL):
  *     rstd_t = 1 / sqrt(mean(s_t^2) + eps),   Y_t = s_t rstd_t gain   (rounded once)

@@ -25,6 +25,8 @@ def test_null_handle_calls(L):
     assert L.ckl_embed_grad(N, N, N, N, 4, 8, 0, 1.0, 0, N, N, 0, N, 0) == 1
     assert L.ckl_act8_pack(N, N, 4, 8, 0, N, N, N) == 1
     assert L.ckl_act8_unpack(N, N, N, 4, 8, 0, N, N) == 1
+    assert L.ckl_act8_weight_grad_workspace_bytes(N, 4, 8, 8, ctypes.byref(n)) == 1
+    assert L.ckl_act8_weight_grad(N, N, 4, 8, N, N, 8, 0, 0, N, N, 0, N, 0) == 1
     assert L.ckl_norm(N, N, N, N, 4, 1e-5, 0, N, N, N, N, N, N) == 1
     assert L.ckl_norm_bwd_workspace_bytes(N, 4, ctypes.byref(n)) == 1
     assert L.ckl_norm_bwd(N, N, N, N, N, N, N, 4, 0, 0, N, N, N, 0, N) == 1
