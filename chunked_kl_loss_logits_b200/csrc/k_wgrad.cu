@@ -13,18 +13,22 @@
 //
 // Work unit: a 256 x 256 tile of dW and a range of tokens, by a CTA pair
 // (tcgen05.mma.cta_group::2), 64 tokens a step. Both operands are MN-major: dY by TMA, X' by
-// four warps of each CTA, each thread one token of 64 columns: 64 bytes of codes and two
-// scale bytes loaded three steps ahead into registers (they need no alignment beyond 8
-// bytes, which a TMA copy would), converted, and stored in the 128-byte swizzle that the MMA
-// reads. The tensor cores cut the running sum at each step instead of rounding it: a relative
+// two groups of four warps of each CTA that take the steps in turn: codes come to shared memory
+// by cp.async (they need no alignment beyond 8 bytes, which a TMA copy would) and scales to
+// registers, four of the group's steps ahead, are converted, and stored in the 128-byte
+// swizzle that the MMA reads. The tensor cores cut the running sum at each step instead of rounding it: a relative
 // error that grows with the number of steps (1e-6 at 2048 tokens, 1.5e-5 at 32768). So a
 // tile's sum is taken out after kFlush steps, and added up in fp32 by the epilogue; the parts
 // of an fp32 dY are contracted smallest first, which keeps their errors as small as they are.
-// Roles, per CTA (320 threads):
+// Roles, per CTA (480 threads):
 //   warp 0      TMA producer of dY (both CTAs; completion on the even CTA's `full`)
 //   warp 1      allocates TMEM; in the even CTA one thread issues the MMAs
 //   warps 2..5  epilogue: the CTA's 128 accumulator rows, while the MMAs fill the other one
-//   warps 6..9  converters (both CTAs; each warp arrives on the even CTA's `full`)
+//   warps 6..13 converters (both CTAs; each warp arrives on its CTA's `conv`)
+//   warp 14     publisher (both CTAs): waits for `conv`, makes the converters' stores visible to
+//               the tensor cores (fence.proxy.async), arrives on the even CTA's `full`. Done by
+//               the converters themselves, the fence waits for the loads they have in flight:
+//               1428 us at 32768 x 2880 x 2880 where the publisher's take 966.
 // Every wait is bounded (common.cuh).
 #include <algorithm>
 #include <atomic>
@@ -40,15 +44,18 @@ namespace {
 constexpr int kBM = 128;                      // dY columns (rows of dW) per CTA
 constexpr int kBK = 64;                       // tokens a step
 constexpr int kBN = 256, kBNH = kBN / 2;      // X' columns of the pair, of a CTA
-constexpr int kStages = 7;
+constexpr int kStages = 5;
 constexpr int kAtom = 64 * 128;               // 64 (MN) x 64 (K) bf16
 constexpr int kABytes = 2 * kAtom, kBBytes = 2 * kAtom, kStageBytes = kABytes + kBBytes;
-constexpr int kWgThreads = 320;
 constexpr int kTmemCols = 512, kAccCols = 256;
-constexpr int kConvWarps = 4;
+constexpr int kConvWarps = 8, kGroups = 2;    // converter warps; groups that take steps in turn
+constexpr int kDepth = 4;                     // steps of its own a group loads ahead
+constexpr int kGroupWarps = kConvWarps / kGroups;
+constexpr int kPass = kBK / (kGroupWarps * 4);  // tokens a converter thread has of a step
+constexpr int kWgThreads = (7 + kConvWarps) * 32;
 constexpr int kFlush = 64;                    // steps (of 64 tokens) one accumulator sums
-constexpr int kAhead = 3;                     // steps the converters load ahead
-constexpr int kWgSmem = 1024 + kStages * kStageBytes + 256;
+constexpr int kRawBytes = kBK * kBNH;         // the codes of a step
+constexpr int kWgSmem = 1024 + kStages * kStageBytes + kGroups * kDepth * kRawBytes + 256;
 static_assert(kWgSmem <= 232448, "shared memory per CTA");
 constexpr uint16_t kPair = 0x3;
 
@@ -60,36 +67,27 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// Arrival that publishes this warp's shared-memory writes to the pair's MMA.
-__device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+// *dst += v in L2, with nothing to wait for. One thread makes all additions to an element, in
+// its program's order, so the sums do not depend on timing.
+__device__ __forceinline__ void red_add4(float4* dst, const float4& v) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w)
                : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+// Copy of N bytes (8 or 16) to shared memory, tracked per thread in groups.
+template <int N>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+  if (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-// As mbar_wait, acquiring at cluster scope.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity,
-                                             volatile int* abort_flag, unsigned* status) {
-  if (try_wait_cluster(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *abort_flag = 1;
-      atomicOr(status, (unsigned)ST_TIMEOUT);
-      return false;
-    }
-  }
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 struct WgTile {
@@ -106,40 +104,43 @@ __device__ __forceinline__ WgTile wg_tile(const WgradArgs& p, int n_m, int n_n, 
   return c;
 }
 
-// A converter thread's share of a step: 64 codes of one token and their two scale bytes.
-struct Codes {
-  uint4 q[4];
-  uint32_t e0, e1;
-};
-
-// V16: rows of codes start on 16-byte boundaries (cols % 16 == 0).
+// 16 codes of a token from column c into shared memory, and their scale. Loads are
+// unconditional (what is past the last token or column reads the last one's); V16: rows of
+// codes start on 16-byte boundaries (cols % 16 == 0).
 template <bool V16>
-__device__ __forceinline__ void load_codes(const WgradArgs& p, int64_t t, int c0, Codes& k) {
-  k.e0 = k.e1 = 1u;  // what is past the rows or columns is 0 * 2^-126
+__device__ __forceinline__ void load_codes(const WgradArgs& p, int64_t t, int c, uint4* dst,
+                                           uint32_t& e) {
+  t = min(t, p.T - 1);
+  const uint8_t* src = p.q + t * p.cols;
+  e = p.e[t * p.nb + min(c >> 5, p.nb - 1)];
+  if (V16) {
+    cp_async<16>(dst, src + min(c, p.cols - 16));
+  } else {
+    cp_async<8>(dst, src + min(c, p.cols - 8));
+    cp_async<8>(reinterpret_cast<uint2*>(dst) + 1, src + min(c + 8, p.cols - 8));
+  }
+}
+
+// Four codes to bf16. int8: a code's byte with its sign bit flipped, in the low bits of
+// 2^23, is 2^23 + 128 + code.
+template <int FMT>
+__device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, float scale) {
+  float f[4];
+  if (FMT == kActInt8) {
+    w ^= 0x80808080u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) k.q[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (t >= p.T || c0 >= p.cols) return;
-  const uint8_t* src = p.q + t * p.cols + c0;
-  const uint8_t* es = p.e + t * p.nb + (c0 >> 5);
-  k.e0 = es[0];
-  if (c0 + 32 < p.cols) k.e1 = es[1];
+    for (int i = 0; i < 4; ++i)
+      f[i] = (__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7550 + i)) - 8388736.f) * scale;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (V16) {
-      if (c0 + 16 * i < p.cols) k.q[i] = *reinterpret_cast<const uint4*>(src + 16 * i);
-    } else {
-      if (c0 + 16 * i < p.cols) {
-        const uint2 a = *reinterpret_cast<const uint2*>(src + 16 * i);
-        k.q[i].x = a.x;
-        k.q[i].y = a.y;
-      }
-      if (c0 + 16 * i + 8 < p.cols) {
-        const uint2 a = *reinterpret_cast<const uint2*>(src + 16 * i + 8);
-        k.q[i].z = a.x;
-        k.q[i].w = a.y;
-      }
+    for (int i = 0; i < 2; ++i) {
+      const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3));
+      const float2 v = __half22float2(h);
+      f[2 * i] = v.x * scale;
+      f[2 * i + 1] = v.y * scale;
     }
   }
+  return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
 }
 
 template <int FMT, bool V16>
@@ -148,9 +149,11 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);  // even CTA's in use
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes +
+                                                kGroups * kDepth * kRawBytes);  // even CTA's in use
   uint64_t* empty = full + kStages;     // both CTAs
-  uint64_t* tfull = empty + kStages;    // [2] both CTAs
+  uint64_t* conv = empty + kStages;     // both CTAs
+  uint64_t* tfull = conv + kStages;     // [2] both CTAs
   uint64_t* tempty = tfull + 2;         // [2] even CTA's in use
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -164,8 +167,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1 + 2 * kConvWarps);  // the byte count of dY, every converter warp
+      mbar_init(&full[s], 1 + 2);  // the byte count of dY, the publishers
       mbar_init(&empty[s], 1);
+      mbar_init(&conv[s], kGroupWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + (uint32_t)(buf * kAccCols);
           for (int kb = kf; kb < min(kf + kFlush, c.kb1); ++kb) {
-            if (!wait_cluster(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+            if (!mbar_wait(&full[stage], phase, abort_flag, p.status)) { ok = false; break; }
             tc_fence_after();
             const uint32_t a0 = smem_u32(smem + stage * kStageBytes), b0 = a0 + kABytes;
   #pragma unroll
@@ -272,23 +276,20 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kAccCols);
         const int row = c.mt * 2 * kBM + (int)rank * kBM + q * 32 + lane;
         float* out = p.out + ((int64_t)c.split * p.n + row) * p.cols;
-  #pragma unroll 1
+#pragma unroll 1
         for (int cc = 0; cc < kBN / 32; ++cc) {
           const int cb = c.nt * kBN + cc * 32;
           if (cb >= p.cols) break;
           float v[32];
           tmem_ld32(taddr + cc * 32, v);
           if (row >= p.n) continue;
-  #pragma unroll
+#pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (cb + 4 * j >= p.cols) break;  // cols % 8 == 0: whole vectors
             float4* dst = reinterpret_cast<float4*>(out + cb + 4 * j);
-            float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            if (add) {
-              const float4 old = *dst;
-              o = make_float4(old.x + o.x, old.y + o.y, old.z + o.z, old.w + o.w);
-            }
-            *dst = o;
+            const float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            if (add) red_add4(dst, o);
+            else *dst = o;
           }
         }
         tc_fence_before();
@@ -296,44 +297,82 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         if (lane == 0) mbar_arrive_cluster(cluster_map(&tempty[buf], 0));
       }
     }
-  } else {
-    // ------------------------------------------------------------ converters
-    const int w = warp - 6, a = w >> 1, r = (w & 1) * 32 + lane;  // atom (64 columns), token
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int tile = pair; ok && tile < n_tiles; tile += n_pairs) {
-      const WgTile c = wg_tile(p, n_m, n_n, tile);
-      const int c0 = c.nt * kBN + (int)rank * kBNH + a * 64;
-      auto fetch = [&](int kb, Codes& k) {
-        if (kb < c.kb1) load_codes<V16>(p, (int64_t)(kb % p.kb_part) * kBK + r, c0, k);
-      };
-      Codes k[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) fetch(c.kb0 + u, k[u]);
-      for (int kb = c.kb0; ok && kb < c.kb1; kb += kAhead) {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (!ok || kb + u >= c.kb1) break;
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
-          uint4* dst = reinterpret_cast<uint4*>(smem + stage * kStageBytes + kABytes + a * kAtom +
-                                                r * 128);
-          const float s0 = act8_scale(k[u].e0), s1 = act8_scale(k[u].e1);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {  // 16-byte chunk j of row r sits at j ^ (r % 8)
-            const uint4 qq = k[u].q[j >> 1];
-            float f[8];
-            act8_decode(j & 1 ? make_uint2(qq.z, qq.w) : make_uint2(qq.x, qq.y), j < 4 ? s0 : s1,
-                        FMT, f);
-            dst[j ^ (r & 7)] = from_f32<uint16_t>(f).u;
-          }
+  } else if (warp == 6 + kConvWarps) {
+    // ------------------------------------------------------------ publisher
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < n_tiles; tile += n_pairs) {
+        const WgTile c = wg_tile(p, n_m, n_n, tile);
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          if (!mbar_wait(&conv[stage], phase, abort_flag, p.status)) { ok = false; break; }
           fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) arrive_release_cluster(cluster_map(&full[stage], 0));
-          fetch(kb + u + kAhead, k[u]);
+          mbar_arrive_cluster(cluster_map(&full[stage], 0));
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
       }
+    }
+  } else {
+    // ------------------------------------------------------------ converters
+    // Group g has every kGroups-th step. Eight neighbouring threads read 128 neighbouring
+    // codes of a token: a thread has 16 of each of the tokens r0, r0 + 4 kGroupWarps, ... and
+    // reads back from shared memory only what it copied there itself.
+    const int g = (warp - 6) / kGroupWarps, ct = threadIdx.x - (6 + g * kGroupWarps) * 32;
+    const int seg = ct & 7, r0 = ct >> 3;
+    uint4* raw = reinterpret_cast<uint4*>(smem + kStages * kStageBytes + g * kDepth * kRawBytes) + ct;
+    unsigned char* dst0 = smem + kABytes + (seg >> 2) * kAtom + r0 * 128;
+    int cnt = 0;  // steps of the tiles before
+    bool ok = true;
+    for (int tile = pair; ok && tile < n_tiles; tile += n_pairs) {
+      const WgTile c = wg_tile(p, n_m, n_n, tile);
+      const int col = c.nt * kBN + (int)rank * kBNH + seg * 16;
+      const int first = c.kb0 + (g - cnt % kGroups + kGroups) % kGroups;
+      uint32_t e[kDepth][kPass];
+      auto token = [&](int kb, int h) {
+        return (int64_t)(kb % p.kb_part) * kBK + r0 + 4 * kGroupWarps * h;
+      };
+      auto slot = [&](int u, int h) { return raw + u * (kRawBytes / 16) + h * 32 * kGroupWarps; };
+      auto fetch = [&](int kb, int u) {
+#pragma unroll
+        for (int h = 0; h < kPass; ++h)
+          load_codes<V16>(p, token(min(kb, c.kb1 - 1), h), col, slot(u, h), e[u][h]);
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int u = 0; u < kDepth; ++u) fetch(first + u * kGroups, u);
+      for (int kb0 = first; ok && kb0 < c.kb1; kb0 += kDepth * kGroups) {
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u) {
+          const int kb = kb0 + u * kGroups;
+          if (!ok || kb >= c.kb1) break;
+          const int at = cnt + kb - c.kb0, stage = at % kStages;
+          const uint32_t phase = (uint32_t)(at / kStages) & 1u;
+          cp_async_wait<kDepth - 1>();
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+#pragma unroll
+          for (int h = 0; h < kPass; ++h) {
+            const bool in = token(kb, h) < p.T;  // past the last token: zeros, as dY has there
+            const float scale = act8_scale(in ? e[u][h] : 1u);
+            const uint4 q = in ? *slot(u, h) : make_uint4(0u, 0u, 0u, 0u);
+            const uint2 a = codes_to_bf16<FMT>(q.x, scale), b = codes_to_bf16<FMT>(q.y, scale);
+            const uint2 d = codes_to_bf16<FMT>(q.z, scale), f = codes_to_bf16<FMT>(q.w, scale);
+            const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, f.x, f.y);
+            // 16-byte chunk i of row r sits at i ^ (r % 8); the second atom's threads store
+            // their halves in the other order, so that eight threads meet eight banks
+            uint4* dst = reinterpret_cast<uint4*>(dst0 + stage * kStageBytes +
+                                                  h * 4 * kGroupWarps * 128);
+            const int i = 2 * (seg & 3), sw = (r0 + 4 * kGroupWarps * h) & 7, odd = seg >> 2;
+            dst[(i + odd) ^ sw] = odd ? hi : lo;
+            dst[(i + 1 - odd) ^ sw] = odd ? lo : hi;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&conv[stage]);
+          fetch(kb + kDepth * kGroups, u);
+        }
+      }
+      cp_async_wait<0>();
+      cnt += c.kb1 - c.kb0;
     }
   }
 
