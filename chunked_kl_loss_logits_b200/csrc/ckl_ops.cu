@@ -69,7 +69,7 @@ ckl_status check_act8(const ckl_ctx* h, int64_t T, int64_t cols, int fmt, const 
 struct WgradPlan {
   int64_t parts = 0, kb_part = 0, n_kb = 0, kb_split = 0;
   int n_split = 1;
-  size_t off_parts = 0, off_sum = 0, total = 0;
+  size_t off_x = 0, off_parts = 0, off_sum = 0, total = 0;
 };
 
 WgradPlan wgrad_plan(const ckl_ctx* h, int64_t T, int64_t n, int64_t cols) {
@@ -81,6 +81,7 @@ WgradPlan wgrad_plan(const ckl_ctx* h, int64_t T, int64_t n, int64_t cols) {
   p.kb_split = (p.n_kb + p.n_split - 1) / p.n_split;
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
+  p.off_x = take((size_t)T * cols * 2);
   if (p.parts > 1) p.off_parts = take((size_t)T * n * 2 * p.parts);
   if (p.n_split > 1) p.off_sum = take((size_t)p.n_split * n * cols * 4);
   p.total = o;
@@ -137,23 +138,27 @@ ckl_status ckl_act8_weight_grad(ckl_handle h, const void* dY, int64_t T, int64_t
             [&] { launch_split3(static_cast<const float*>(dY), T * n, parts, s); }));
       a = parts;
     }
-    CUtensorMap map;
-    if (!make_map_planes(h, &map, a, n, T, P.parts)) return CKL_ERR_CUDA;
+    void* x = base + P.off_x;
+    chk(L(KID_ACT8_UNPACK, 0, (double)T * cols * (2.0 + 33.0 / 32), [&] {
+      launch_act8_unpack(true, static_cast<const uint8_t*>(q), scale, T, (int)cols, fmt, x, s);
+    }));
+    float* out = P.n_split > 1 ? reinterpret_cast<float*>(base + P.off_sum) : dW;
+    CUtensorMap ma, mb, mc;
+    if (!make_map_planes(h, &ma, a, n, T, P.parts, 64) ||
+        !make_map(h, &mb, x, cols, T, (uint64_t)cols * 2, 64, 64) ||
+        !make_map_planes(h, &mc, out, cols, n, P.n_split, 32, true))
+      return CKL_ERR_CUDA;
     WgradArgs p{};
-    p.q = static_cast<const uint8_t*>(q);
-    p.e = scale;
-    p.T = T;
-    p.n = (int)n; p.cols = (int)cols; p.nb = (int)((cols + 31) / 32);
+    p.n = (int)n; p.cols = (int)cols;
     p.kb_part = (int)P.kb_part; p.n_kb = (int)P.n_kb;
     p.n_split = P.n_split; p.kb_split = (int)P.kb_split;
     p.add = P.n_split == 1 && accumulate;
-    p.out = P.n_split > 1 ? reinterpret_cast<float*>(base + P.off_sum) : dW;
     p.status = h->d_status;
     chk(L(KID_WGRAD, 2.0 * T * n * cols, 0,
-          [&] { chk(launch_wgrad(map, p, fmt, h->num_sms, s)); }));
+          [&] { chk(launch_wgrad(ma, mb, mc, p, h->num_sms, s)); }));
     if (P.n_split > 1)
       chk(L(KID_WGRAD_SUM, 0, 4.0 * n * cols * (P.n_split + 1),
-            [&] { launch_wgrad_sum(p.out, P.n_split, n * cols, accumulate != 0, dW, s); }));
+            [&] { launch_wgrad_sum(out, P.n_split, n * cols, accumulate != 0, dW, s); }));
   }
   if ((st = cuda_status(err)) != CKL_OK) return st;
   return wait ? sync_and_read(h, s, nullptr, nullptr) : CKL_OK;

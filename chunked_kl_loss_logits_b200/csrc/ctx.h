@@ -105,16 +105,18 @@ inline bool make_map(const ckl_ctx* h, CUtensorMap* m, const void* base, uint64_
   return r == CUDA_SUCCESS;
 }
 
-// 3-D bf16 tensor map of `outer` planes of rows x inner, dense; boxes of 64 x 64 x 1, 128-byte
-// swizzle, zero fill outside.
+// 3-D tensor map (bf16, or fp32 when f32 is set) of `outer` planes of rows x inner, dense;
+// boxes of box x box x 1, 128-byte swizzle, zero fill outside (loads) / clipping (stores).
 inline bool make_map_planes(const ckl_ctx* h, CUtensorMap* m, const void* base, uint64_t inner,
-                            uint64_t rows, uint64_t outer) {
+                            uint64_t rows, uint64_t outer, uint32_t box, bool f32 = false) {
+  const uint64_t es = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {inner, rows, outer};
-  const cuuint64_t strides[2] = {inner * 2, inner * rows * 2};
-  const cuuint32_t box[3] = {64, 64, 1};
+  const cuuint64_t strides[2] = {inner * es, inner * rows * es};
+  const cuuint32_t boxes[3] = {box, box, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return h->encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                   const_cast<void*>(base), dims, strides, boxes, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

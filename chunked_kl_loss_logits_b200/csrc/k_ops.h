@@ -62,20 +62,19 @@ void launch_norm_dgain(const float* part, int64_t rows, int d, bool accumulate, 
 
 // ---- weight gradient from a checkpoint (k_wgrad.cu)
 struct WgradArgs {
-  const uint8_t *q, *e;
-  int64_t T;
-  int n, cols, nb;  // dY columns, X' columns, blocks of a row of X'
+  int n, cols;      // dY columns, X' columns
   int kb_part;      // 64-token steps of one part of dY
   int n_kb;         // steps in all (parts x kb_part)
   int n_split, kb_split;
-  int add;          // add to out (n_split == 1 only)
-  float* out;       // n x cols, or n_split partial results of that size
+  int add;          // add to the result (n_split == 1 only)
   unsigned* status;
 };
 int wgrad_split(int64_t n, int64_t cols, int64_t n_kb, int num_sms);
-// a: the bf16 parts of dY as a (n, T, parts) tensor, boxes of 64 x 64 x 1
-cudaError_t launch_wgrad(const CUtensorMap& a, const WgradArgs& p, int fmt, int num_sms,
-                         cudaStream_t s);
+// a: the bf16 parts of dY as a (n, T, parts) tensor, boxes of 64 x 64 x 1; b: X' in bf16 as
+// a (cols, T) tensor, boxes of 64 x 64; c: dW or the n_split partial results as an fp32
+// (cols, n, n_split) tensor, boxes of 32 x 32 x 1
+cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
+                         const WgradArgs& p, int num_sms, cudaStream_t s);
 void launch_split3(const float* x, int64_t n, uint16_t* out, cudaStream_t s);
 void launch_wgrad_sum(const float* part, int n_split, int64_t n, bool add, float* out,
                       cudaStream_t s);

@@ -2,34 +2,30 @@
 //
 //     dW[n][c] (+)= sum_t dY[t][n] X'[t][c],    X'[t][c] = code[t][c] * 2^e[t][c / 32]
 //
-// on the tensor cores, the codes turned into bf16 on their way into shared memory. X' has
-// at most 8 significant bits, so bf16 holds it exactly. bf16 dY enters as it is; fp32 dY is
-// cut into three bf16 parts of 8 bits each (their sum is dY exactly) that are contracted one
-// after the other, so both types get exact products and fp32 sums.
+// on the tensor cores. X' has at most 8 significant bits, so bf16 holds it exactly: it is
+// unpacked to a bf16 workspace first. bf16 dY enters as it is; fp32 dY is cut into three bf16
+// parts of 8 bits each (their sum is dY exactly) that are contracted one after the other, so
+// both types get exact products and fp32 sums.
 //
 // Bound by the tensor cores: 2 T n c operations (three times that for fp32) against T (2n + c)
-// bytes, a thousand operations a byte at n = c = 2880. Reading the codes in the contraction
-// instead of a bf16 copy saves writing that copy and reading it back (4 T c bytes).
+// bytes, a thousand operations a byte at n = c = 2880.
 //
 // Work unit: a 256 x 256 tile of dW and a range of tokens, by a CTA pair
-// (tcgen05.mma.cta_group::2), 64 tokens a step. Both operands are MN-major: dY by TMA, X' by
-// two groups of four warps of each CTA that take the steps in turn: codes come to shared memory
-// by cp.async (they need no alignment beyond 8 bytes, which a TMA copy would) and scales to
-// registers, four of the group's steps ahead, are converted, and stored in the 128-byte
-// swizzle that the MMA reads. The tensor cores cut the running sum at each step instead of rounding it: a relative
-// error that grows with the number of steps (1e-6 at 2048 tokens, 1.5e-5 at 32768). So a
-// tile's sum is taken out after kFlush steps, and added up in fp32 by the epilogue; the parts
-// of an fp32 dY are contracted smallest first, which keeps their errors as small as they are.
-// Roles, per CTA (480 threads):
-//   warp 0      TMA producer of dY (both CTAs; completion on the even CTA's `full`)
+// (tcgen05.mma.cta_group::2), 64 tokens a step. Both operands are MN-major as they lie in
+// memory, and come by TMA. The tensor cores cut the running sum at each step instead of
+// rounding it: a relative error that grows with the number of steps (1e-6 at 2048 tokens,
+// 1.5e-5 at 32768). So a tile's sum is taken out after kFlush steps and added up in fp32 by
+// the epilogue; the parts of an fp32 dY are contracted smallest first, which keeps their
+// errors as small as they are. Roles, per CTA (192 threads):
+//   warp 0      TMA producer (both CTAs; completion on the even CTA's `full`)
 //   warp 1      allocates TMEM; in the even CTA one thread issues the MMAs
 //   warps 2..5  epilogue: the CTA's 128 accumulator rows, while the MMAs fill the other one
-//   warps 6..13 converters (both CTAs; each warp arrives on its CTA's `conv`)
-//   warp 14     publisher (both CTAs): waits for `conv`, makes the converters' stores visible to
-//               the tensor cores (fence.proxy.async), arrives on the even CTA's `full`. Done by
-//               the converters themselves, the fence waits for the loads they have in flight:
-//               1428 us at 32768 x 2880 x 2880 where the publisher's take 966.
 // Every wait is bounded (common.cuh).
+//
+// Converting the codes inside the contraction (by further warps, from the codes in shared
+// memory or in registers) was measured and not kept: 560 us at 32768 x 2880 x 2880. The
+// extra passes over shared memory (codes in and out, bf16 in) take bandwidth that the MMA
+// needs for its operands; unpacking first moves 3 bytes a code through HBM and L2 instead.
 #include <algorithm>
 #include <atomic>
 
@@ -44,18 +40,14 @@ namespace {
 constexpr int kBM = 128;                      // dY columns (rows of dW) per CTA
 constexpr int kBK = 64;                       // tokens a step
 constexpr int kBN = 256, kBNH = kBN / 2;      // X' columns of the pair, of a CTA
-constexpr int kStages = 5;
+constexpr int kStages = 6;
 constexpr int kAtom = 64 * 128;               // 64 (MN) x 64 (K) bf16
 constexpr int kABytes = 2 * kAtom, kBBytes = 2 * kAtom, kStageBytes = kABytes + kBBytes;
+constexpr int kWgThreads = 192;
 constexpr int kTmemCols = 512, kAccCols = 256;
-constexpr int kConvWarps = 8, kGroups = 2;    // converter warps; groups that take steps in turn
-constexpr int kDepth = 4;                     // steps of its own a group loads ahead
-constexpr int kGroupWarps = kConvWarps / kGroups;
-constexpr int kPass = kBK / (kGroupWarps * 4);  // tokens a converter thread has of a step
-constexpr int kWgThreads = (7 + kConvWarps) * 32;
 constexpr int kFlush = 64;                    // steps (of 64 tokens) one accumulator sums
-constexpr int kRawBytes = kBK * kBNH;         // the codes of a step
-constexpr int kWgSmem = 1024 + kStages * kStageBytes + kGroups * kDepth * kRawBytes + 256;
+constexpr int kBox = 32 * 128;                // a staged 32 x 32 fp32 box of an epilogue warp
+constexpr int kWgSmem = 1024 + kStages * kStageBytes + 4 * 2 * kBox + 256;
 static_assert(kWgSmem <= 232448, "shared memory per CTA");
 constexpr uint16_t kPair = 0x3;
 
@@ -67,27 +59,22 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// *dst += v in L2, with nothing to wait for. One thread makes all additions to an element, in
-// its program's order, so the sums do not depend on timing.
-__device__ __forceinline__ void red_add4(float4* dst, const float4& v) {
-  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
-               : "memory");
-}
-// Copy of N bytes (8 or 16) to shared memory, tracked per thread in groups.
-template <int N>
-__device__ __forceinline__ void cp_async(void* dst, const void* src) {
-  if (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// Store or add a staged box at (column c0, row c1) of plane c2; rows and columns outside are
+// not written.
+__device__ __forceinline__ void tma_put_3d(const CUtensorMap* m, const void* src, int c0, int c1,
+                                           int c2, bool add) {
+  if (add)
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+        " [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(m)),
+        "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+            reinterpret_cast<uint64_t>(m)),
+        "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
 }
 
 struct WgTile {
@@ -104,56 +91,16 @@ __device__ __forceinline__ WgTile wg_tile(const WgradArgs& p, int n_m, int n_n, 
   return c;
 }
 
-// 16 codes of a token from column c into shared memory, and their scale. Loads are
-// unconditional (what is past the last token or column reads the last one's); V16: rows of
-// codes start on 16-byte boundaries (cols % 16 == 0).
-template <bool V16>
-__device__ __forceinline__ void load_codes(const WgradArgs& p, int64_t t, int c, uint4* dst,
-                                           uint32_t& e) {
-  t = min(t, p.T - 1);
-  const uint8_t* src = p.q + t * p.cols;
-  e = p.e[t * p.nb + min(c >> 5, p.nb - 1)];
-  if (V16) {
-    cp_async<16>(dst, src + min(c, p.cols - 16));
-  } else {
-    cp_async<8>(dst, src + min(c, p.cols - 8));
-    cp_async<8>(reinterpret_cast<uint2*>(dst) + 1, src + min(c + 8, p.cols - 8));
-  }
-}
-
-// Four codes to bf16. int8: a code's byte with its sign bit flipped, in the low bits of
-// 2^23, is 2^23 + 128 + code.
-template <int FMT>
-__device__ __forceinline__ uint2 codes_to_bf16(uint32_t w, float scale) {
-  float f[4];
-  if (FMT == kActInt8) {
-    w ^= 0x80808080u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f[i] = (__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7550 + i)) - 8388736.f) * scale;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3));
-      const float2 v = __half22float2(h);
-      f[2 * i] = v.x * scale;
-      f[2 * i + 1] = v.y * scale;
-    }
-  }
-  return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-}
-
-template <int FMT, bool V16>
 __global__ void __launch_bounds__(kWgThreads, 1)
-    wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const WgradArgs p) {
+    wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmC, const WgradArgs p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes +
-                                                kGroups * kDepth * kRawBytes);  // even CTA's in use
+  unsigned char* boxes = smem + kStages * kStageBytes;  // [4 warps][2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 4 * 2 * kBox);  // even CTA's in use
   uint64_t* empty = full + kStages;     // both CTAs
-  uint64_t* conv = empty + kStages;     // both CTAs
-  uint64_t* tfull = conv + kStages;     // [2] both CTAs
+  uint64_t* tfull = empty + kStages;    // [2] both CTAs
   uint64_t* tempty = tfull + 2;         // [2] even CTA's in use
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -167,9 +114,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1 + 2);  // the byte count of dY, the publishers
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&conv[s], kGroupWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -179,7 +125,11 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 0 && lane == 0) tma_prefetch_desc(&tmA);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmC);
+  }
   if (warp == 1) tmem_alloc_pair(tmem_slot, kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -188,23 +138,26 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ dY producer
+    // ------------------------------------------------------------ producer
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
       for (int tile = pair; ok && tile < n_tiles; tile += n_pairs) {
         const WgTile c = wg_tile(p, n_m, n_n, tile);
-        const int row0 = c.mt * 2 * kBM + (int)rank * kBM;
+        const int row0 = c.mt * 2 * kBM + (int)rank * kBM, col0 = c.nt * kBN + (int)rank * kBNH;
         for (int kb = c.kb0; kb < c.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
           unsigned char* sA = smem + stage * kStageBytes;
           const uint32_t fbar = cluster_map(&full[stage], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kABytes);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
           const int part = kb / p.kb_part, t0 = (kb - part * p.kb_part) * kBK;
 #pragma unroll
           for (int a = 0; a < 2; ++a)
             tma_load_3d_pair(sA + a * kAtom, &tmA, fbar, row0 + a * 64, t0, part);
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+            tma_load_2d_pair(sA + kABytes + a * kAtom, &tmB, fbar, col0 + a * 64, t0);
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
@@ -258,13 +211,15 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         if (clock64() - t0 > kWaitCycles) { atomicOr(p.status, (unsigned)ST_TIMEOUT); break; }
       }
     }
-  } else if (warp < 6) {
+  } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // TMEM lane quarter this warp may access
-    int it = 0;
+    unsigned char* mine = boxes + q * 2 * kBox;
+    int it = 0, filled = 0;
     bool ok = true;
     for (int tile = pair; ok && tile < n_tiles; tile += n_pairs) {
       const WgTile c = wg_tile(p, n_m, n_n, tile);
+      const int row0 = c.mt * 2 * kBM + (int)rank * kBM + q * 32;  // this warp's rows of dW
       for (int kf = c.kb0; kf < c.kb1; kf += kFlush, ++it) {
         const int buf = it & 1;
         if (!mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, p.status)) {
@@ -274,22 +229,28 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         tc_fence_after();
         const bool add = p.add || kf > c.kb0;
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kAccCols);
-        const int row = c.mt * 2 * kBM + (int)rank * kBM + q * 32 + lane;
-        float* out = p.out + ((int64_t)c.split * p.n + row) * p.cols;
+        // this tile's earlier sum is in place: additions to an element keep their order
+        if (lane == 0) bulk_wait_all();
 #pragma unroll 1
         for (int cc = 0; cc < kBN / 32; ++cc) {
           const int cb = c.nt * kBN + cc * 32;
-          if (cb >= p.cols) break;
+          if (cb >= p.cols || row0 >= p.n) break;
           float v[32];
           tmem_ld32(taddr + cc * 32, v);
-          if (row >= p.n) continue;
+          unsigned char* box = mine + (filled++ & 1) * kBox;
+          if (lane == 0) bulk_wait_read<1>();  // the box's previous contents have been read
+          __syncwarp();
+          uint4* rowp = reinterpret_cast<uint4*>(box + lane * 128);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (cb + 4 * j >= p.cols) break;  // cols % 8 == 0: whole vectors
-            float4* dst = reinterpret_cast<float4*>(out + cb + 4 * j);
-            const float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            if (add) red_add4(dst, o);
-            else *dst = o;
+          for (int j = 0; j < 8; ++j)
+            rowp[j ^ (lane & 7)] = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                              __float_as_uint(v[4 * j + 2]),
+                                              __float_as_uint(v[4 * j + 3]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_put_3d(&tmC, box, cb, row0, c.split, add);
+            bulk_commit();
           }
         }
         tc_fence_before();
@@ -297,83 +258,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         if (lane == 0) mbar_arrive_cluster(cluster_map(&tempty[buf], 0));
       }
     }
-  } else if (warp == 6 + kConvWarps) {
-    // ------------------------------------------------------------ publisher
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int tile = pair; ok && tile < n_tiles; tile += n_pairs) {
-        const WgTile c = wg_tile(p, n_m, n_n, tile);
-        for (int kb = c.kb0; kb < c.kb1; ++kb) {
-          if (!mbar_wait(&conv[stage], phase, abort_flag, p.status)) { ok = false; break; }
-          fence_proxy_async_smem();
-          mbar_arrive_cluster(cluster_map(&full[stage], 0));
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
-        }
-      }
-    }
-  } else {
-    // ------------------------------------------------------------ converters
-    // Group g has every kGroups-th step. Eight neighbouring threads read 128 neighbouring
-    // codes of a token: a thread has 16 of each of the tokens r0, r0 + 4 kGroupWarps, ... and
-    // reads back from shared memory only what it copied there itself.
-    const int g = (warp - 6) / kGroupWarps, ct = threadIdx.x - (6 + g * kGroupWarps) * 32;
-    const int seg = ct & 7, r0 = ct >> 3;
-    uint4* raw = reinterpret_cast<uint4*>(smem + kStages * kStageBytes + g * kDepth * kRawBytes) + ct;
-    unsigned char* dst0 = smem + kABytes + (seg >> 2) * kAtom + r0 * 128;
-    int cnt = 0;  // steps of the tiles before
-    bool ok = true;
-    for (int tile = pair; ok && tile < n_tiles; tile += n_pairs) {
-      const WgTile c = wg_tile(p, n_m, n_n, tile);
-      const int col = c.nt * kBN + (int)rank * kBNH + seg * 16;
-      const int first = c.kb0 + (g - cnt % kGroups + kGroups) % kGroups;
-      uint32_t e[kDepth][kPass];
-      auto token = [&](int kb, int h) {
-        return (int64_t)(kb % p.kb_part) * kBK + r0 + 4 * kGroupWarps * h;
-      };
-      auto slot = [&](int u, int h) { return raw + u * (kRawBytes / 16) + h * 32 * kGroupWarps; };
-      auto fetch = [&](int kb, int u) {
-#pragma unroll
-        for (int h = 0; h < kPass; ++h)
-          load_codes<V16>(p, token(min(kb, c.kb1 - 1), h), col, slot(u, h), e[u][h]);
-        cp_async_commit();
-      };
-#pragma unroll
-      for (int u = 0; u < kDepth; ++u) fetch(first + u * kGroups, u);
-      for (int kb0 = first; ok && kb0 < c.kb1; kb0 += kDepth * kGroups) {
-#pragma unroll
-        for (int u = 0; u < kDepth; ++u) {
-          const int kb = kb0 + u * kGroups;
-          if (!ok || kb >= c.kb1) break;
-          const int at = cnt + kb - c.kb0, stage = at % kStages;
-          const uint32_t phase = (uint32_t)(at / kStages) & 1u;
-          cp_async_wait<kDepth - 1>();
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
-#pragma unroll
-          for (int h = 0; h < kPass; ++h) {
-            const bool in = token(kb, h) < p.T;  // past the last token: zeros, as dY has there
-            const float scale = act8_scale(in ? e[u][h] : 1u);
-            const uint4 q = in ? *slot(u, h) : make_uint4(0u, 0u, 0u, 0u);
-            const uint2 a = codes_to_bf16<FMT>(q.x, scale), b = codes_to_bf16<FMT>(q.y, scale);
-            const uint2 d = codes_to_bf16<FMT>(q.z, scale), f = codes_to_bf16<FMT>(q.w, scale);
-            const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, f.x, f.y);
-            // 16-byte chunk i of row r sits at i ^ (r % 8); the second atom's threads store
-            // their halves in the other order, so that eight threads meet eight banks
-            uint4* dst = reinterpret_cast<uint4*>(dst0 + stage * kStageBytes +
-                                                  h * 4 * kGroupWarps * 128);
-            const int i = 2 * (seg & 3), sw = (r0 + 4 * kGroupWarps * h) & 7, odd = seg >> 2;
-            dst[(i + odd) ^ sw] = odd ? hi : lo;
-            dst[(i + 1 - odd) ^ sw] = odd ? lo : hi;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&conv[stage]);
-          fetch(kb + kDepth * kGroups, u);
-        }
-      }
-      cp_async_wait<0>();
-      cnt += c.kb1 - c.kb0;
-    }
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -424,37 +309,6 @@ __global__ void __launch_bounds__(256)
   out[i] = s;
 }
 
-template <int FMT, bool V16>
-cudaError_t launch_one(const CUtensorMap& a, const WgradArgs& p, int num_sms, cudaStream_t s) {
-  const int n_tiles = (p.n + 2 * kBM - 1) / (2 * kBM) * ((p.cols + kBN - 1) / kBN) * p.n_split;
-  static std::atomic<uint64_t> attr_set{0};
-  cudaError_t e = smem_once(wgrad_kernel<FMT, V16>, kWgSmem, attr_set);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kWgThreads, 1, 1);
-  cfg.dynamicSmemBytes = kWgSmem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  // As many pairs as can be resident at once (cached; concurrent first calls agree).
-  static std::atomic<int> cached_pairs{0};
-  int pairs = cached_pairs.load(std::memory_order_relaxed);
-  if (pairs == 0) {
-    cfg.gridDim = dim3((unsigned)(2 * num_sms), 1, 1);
-    if (cudaOccupancyMaxActiveClusters(&pairs, wgrad_kernel<FMT, V16>, &cfg) != cudaSuccess ||
-        pairs < 1)
-      pairs = std::max(1, num_sms / 2);
-    cached_pairs.store(pairs, std::memory_order_relaxed);
-  }
-  cfg.gridDim = dim3((unsigned)(2 * std::min(n_tiles, pairs)), 1, 1);
-  return cudaLaunchKernelEx(&cfg, wgrad_kernel<FMT, V16>, a, p);
-}
-
 }  // namespace
 
 // Splits of the tokens: enough that the tiles fill the pairs evenly, weighed against writing
@@ -474,14 +328,35 @@ int wgrad_split(int64_t n, int64_t cols, int64_t n_kb, int num_sms) {
   return (int)((n_kb + kps - 1) / kps);
 }
 
-cudaError_t launch_wgrad(const CUtensorMap& a, const WgradArgs& p, int fmt, int num_sms,
-                         cudaStream_t s) {
-  const bool v16 = p.cols % 16 == 0;
-  if (fmt == kActInt8)
-    return v16 ? launch_one<kActInt8, true>(a, p, num_sms, s)
-               : launch_one<kActInt8, false>(a, p, num_sms, s);
-  return v16 ? launch_one<kActE4m3, true>(a, p, num_sms, s)
-             : launch_one<kActE4m3, false>(a, p, num_sms, s);
+cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
+                         const WgradArgs& p, int num_sms, cudaStream_t s) {
+  const int n_tiles = (p.n + 2 * kBM - 1) / (2 * kBM) * ((p.cols + kBN - 1) / kBN) * p.n_split;
+  static std::atomic<uint64_t> attr_set{0};
+  cudaError_t e = smem_once(wgrad_kernel, kWgSmem, attr_set);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kWgThreads, 1, 1);
+  cfg.dynamicSmemBytes = kWgSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // As many pairs as can be resident at once (cached; concurrent first calls agree).
+  static std::atomic<int> cached_pairs{0};
+  int pairs = cached_pairs.load(std::memory_order_relaxed);
+  if (pairs == 0) {
+    cfg.gridDim = dim3((unsigned)(2 * num_sms), 1, 1);
+    if (cudaOccupancyMaxActiveClusters(&pairs, wgrad_kernel, &cfg) != cudaSuccess ||
+        pairs < 1)
+      pairs = std::max(1, num_sms / 2);
+    cached_pairs.store(pairs, std::memory_order_relaxed);
+  }
+  cfg.gridDim = dim3((unsigned)(2 * std::min(n_tiles, pairs)), 1, 1);
+  return cudaLaunchKernelEx(&cfg, wgrad_kernel, a, b, c, p);
 }
 
 void launch_split3(const float* x, int64_t n, uint16_t* out, cudaStream_t s) {
