@@ -8,6 +8,7 @@ not been built the import of `lib()` raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -221,6 +222,23 @@ def torch_vocab_group(V_total: int, group=None) -> VocabGroup:
 
 ACT8_FORMATS = {"int8": 0, "e4m3": 1}
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)  # the current stream's handle
+
+
+def _on_stream(method):
+    """Adds `stream` to a method of a handle: the call runs, and what it allocates is allocated,
+    on that stream of the handle's device (by default on its current stream)."""
+    @functools.wraps(method)
+    def call(self, *args, stream=None, **kw):
+        if stream is None:
+            return method(self, *args, **kw)
+        if stream.device.index != self._index:
+            raise ValueError("stream must be one of the handle's device")
+        with torch.cuda.stream(stream):
+            return method(self, *args, **kw)
+    return call
+
 
 class Act8:
     """An 8-bit activation checkpoint: codes q (T x cols, uint8), one power-of-two scale per
@@ -241,6 +259,12 @@ class Act8:
             if not t.is_contiguous() or t.device != q.device:
                 raise ValueError("q, scale and rstd must be contiguous tensors on one device")
         self.q, self.scale, self.fmt, self.rstd = q, scale, fmt, rstd
+
+    @classmethod
+    def _of(cls, q, scale, fmt, rstd):  # parts this module made
+        self = cls.__new__(cls)
+        self.q, self.scale, self.fmt, self.rstd = q, scale, fmt, rstd
+        return self
 
     @property
     def nbytes(self) -> int:
@@ -263,7 +287,7 @@ class ChunkedKL:
         _check(lib().ckl_create(ctypes.byref(h), dev.index or 0,
                                 F32 if dtype == torch.float32 else BF16, V, d, K, max_chunk),
                "ckl_create")
-        self._h = h
+        self._h, self._lib, self._index, self._ws_bytes = h, lib(), dev.index or 0, {}
 
     def close(self):
         if getattr(self, "_h", None):
@@ -497,212 +521,259 @@ class ChunkedKL:
         return idx, logit
 
     # ------------------------------------------------------------------ operators around the loss
-    def _dense(self, *tensors):
-        for t in tensors:
-            if t is not None and (not t.is_contiguous() or t.device != self.device):
-                raise ValueError("inputs must be contiguous tensors on the handle's device")
-
-    def _rows(self, name, t, shape=None):
-        if t.dtype != self.dtype:
+    # These calls are short, so their checks cost what the kernels of a small step do: plain
+    # comparisons, integers for pointers, sizes asked for once.
+    def _rows(self, name, t, *shape):
+        """t is a dense tensor of the handle's dtype on its device, of this shape if given."""
+        if t.dtype is not self.dtype:
             raise TypeError(f"{name} must be {self.dtype}")
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have the shape {tuple(shape)}")
-        self._dense(t)
+        self._dense(name, t, *shape)
+
+    def _f32(self, name, t, *shape):
+        if t.dtype is not torch.float32 or t.shape != shape:
+            raise TypeError(f"{name} must be a float32 tensor of shape {shape}")
+        self._dense(name, t)
+
+    def _dense(self, name, t, *shape):
+        if shape and t.shape != shape:
+            raise ValueError(f"{name} must have the shape {shape}")
+        if not t.is_contiguous() or t.get_device() != self._index:
+            raise ValueError(f"{name} must be a contiguous tensor on the handle's device")
 
     def _ids(self, ids, mask):
-        if ids.dtype != torch.int32:
+        if ids.dtype is not torch.int32:
             raise TypeError("ids must be int32")
-        if mask is not None and (mask.dtype != torch.uint8 or mask.numel() != ids.numel()):
+        self._dense("ids", ids)
+        if mask is None:
+            return None
+        if mask.dtype is not torch.uint8 or mask.numel() != ids.numel():
             raise TypeError("mask must be a uint8 tensor with an entry for each id")
-        self._dense(ids, mask)
+        self._dense("mask", mask)
+        return mask.data_ptr()
 
-    def _workspace(self, query, *args) -> torch.Tensor:
-        n = _SZ()
-        _check(getattr(lib(), query)(self._h, *args, ctypes.byref(n)), query)
-        return torch.empty(n.value, dtype=torch.uint8, device=self.device)
+    def _ckpt(self, ckpt: Act8, rows=None, cols=None) -> int:
+        T, c = ckpt.q.shape
+        if (rows is not None and T != rows) or (cols is not None and c != cols):
+            raise ValueError(f"the checkpoint must be {rows if rows is not None else T} x "
+                             f"{cols if cols is not None else c}")
+        if ckpt.q.get_device() != self._index:
+            raise ValueError("the checkpoint must be on the handle's device")
+        return ACT8_FORMATS[ckpt.fmt]
 
-    def _stream(self, stream):
-        s = stream or torch.cuda.current_stream(self.device)
-        return ctypes.c_void_p(s.cuda_stream)
+    def _new_act8(self, T, cols, fmt, rstd) -> Act8:
+        dev = self.device
+        return Act8._of(torch.empty(T, cols, dtype=torch.uint8, device=dev),
+                        torch.empty(T, (cols + 31) // 32, dtype=torch.uint8, device=dev), fmt,
+                        torch.empty(T, dtype=torch.float32, device=dev) if rstd else None)
 
+    def _workspace(self, query, *sizes) -> torch.Tensor:
+        """A workspace of the size that the library's `query` gives for these sizes."""
+        key = (query, *sizes)
+        n = self._ws_bytes.get(key)
+        if n is None:
+            out = _SZ()
+            _check(getattr(lib(), query)(self._h, *sizes, ctypes.byref(out)), query)
+            if len(self._ws_bytes) >= 256:
+                self._ws_bytes.clear()
+            n = self._ws_bytes[key] = out.value
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def _given(self, workspace):
+        if workspace.dtype is not torch.uint8:
+            raise TypeError("workspace must be uint8")
+        self._dense("workspace", workspace)
+        return workspace
+
+    @_on_stream
     def embed(self, ids, W, mask=None, scale: float = 1.0, V_total: int | None = None, v0: int = 0,
-              out=None, sync: bool = True, stream=None):
+              out=None, sync: bool = True):
         """scale * W[ids - v0] in the handle's dtype (ids' shape, then d): zeros for tokens with
         mask 0 and for ids in [0, V_total) whose row is not among the handle's V (v0 ..)."""
-        self._ids(ids, mask)
-        self._rows("W", W, (self.V, self.d))
-        shape = tuple(ids.shape) + (self.d,)
+        m = self._ids(ids, mask)
+        self._rows("W", W, self.V, self.d)
         if out is None:
-            out = torch.empty(shape, dtype=self.dtype, device=self.device)
-        self._rows("out", out, shape)
-        _check(lib().ckl_embed(self._h, _ptr(ids), _ptr(mask), _ptr(W), ids.numel(),
-                               self.V if V_total is None else V_total, v0, scale, _ptr(out),
-                               self._stream(stream), int(sync)), "ckl_embed")
+            out = torch.empty(*ids.shape, self.d, dtype=self.dtype, device=self.device)
+        else:
+            self._rows("out", out, *ids.shape, self.d)
+        code = self._lib.ckl_embed(self._h, ids.data_ptr(), m, W.data_ptr(), ids.numel(),
+                                   self.V if V_total is None else V_total, v0, scale,
+                                   out.data_ptr(), _raw_stream(self._index), sync)
+        _check(code, "ckl_embed")
         return out
 
+    @_on_stream
     def embed_vocab_parallel(self, group: VocabGroup, ids, W_shard, mask=None, scale: float = 1.0,
-                             sync: bool = True, stream=None):
+                             sync: bool = True):
         """As embed with W split by vocabulary rows over `group`: the full rows on every rank
         (one all-reduce)."""
-        self._ids(ids, mask)
-        self._rows("W_shard", W_shard, (self.V, self.d))
-        out = torch.empty(tuple(ids.shape) + (self.d,), dtype=self.dtype, device=self.device)
+        m = self._ids(ids, mask)
+        self._rows("W_shard", W_shard, self.V, self.d)
+        out = torch.empty(*ids.shape, self.d, dtype=self.dtype, device=self.device)
         ws = self._workspace("ckl_embed_vp_workspace_bytes", ids.numel())
         g, keep = group._c(self.device)
         group.error = None
-        code = lib().ckl_embed_vocab_parallel(self._h, ctypes.byref(g), _ptr(ids), _ptr(mask),
-                                              _ptr(W_shard), ids.numel(), scale, _ptr(out),
-                                              _ptr(ws), ws.numel(), self._stream(stream), int(sync))
+        code = self._lib.ckl_embed_vocab_parallel(
+            self._h, ctypes.byref(g), ids.data_ptr(), m, W_shard.data_ptr(), ids.numel(), scale,
+            out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(self._index), sync)
         del keep
         if code == 9 and group.error is not None:
             raise CKLError(code, "ckl_embed_vocab_parallel") from group.error
         _check(code, "ckl_embed_vocab_parallel")
         return out
 
+    @_on_stream
     def embed_grad(self, ids, dX, mask=None, scale: float = 1.0, V_total: int | None = None,
                    v0: int = 0, dW=None, accumulate: bool = False, workspace=None,
-                   sync: bool = True, stream=None):
+                   sync: bool = True):
         """dW (V x d, float32) of embed: the given buffer, added to with accumulate=True (a tied
         head's dW from fwd_bwd) and overwritten otherwise, or a new one."""
-        self._ids(ids, mask)
-        self._rows("dX", dX, tuple(ids.shape) + (self.d,))
+        m = self._ids(ids, mask)
+        self._rows("dX", dX, *ids.shape, self.d)
         if dW is None:
             if accumulate:
                 raise ValueError("accumulate needs dW")
-            dW = torch.empty((self.V, self.d), dtype=torch.float32, device=self.device)
-        self._f32("dW", dW, (self.V, self.d))
-        ws = workspace if workspace is not None else \
-            self._workspace("ckl_embed_grad_workspace_bytes", ids.numel())
-        _check(lib().ckl_embed_grad(self._h, _ptr(ids), _ptr(mask), _ptr(dX), ids.numel(),
-                                    self.V if V_total is None else V_total, v0, scale,
-                                    int(accumulate), _ptr(dW), _ptr(ws), ws.numel(),
-                                    self._stream(stream), int(sync)), "ckl_embed_grad")
+            dW = torch.empty(self.V, self.d, dtype=torch.float32, device=self.device)
+        else:
+            self._f32("dW", dW, self.V, self.d)
+        T = ids.numel()
+        ws = self._workspace("ckl_embed_grad_workspace_bytes", T) if workspace is None else \
+            self._given(workspace)
+        code = self._lib.ckl_embed_grad(
+            self._h, ids.data_ptr(), m, dX.data_ptr(), T, self.V if V_total is None else V_total,
+            v0, scale, accumulate, dW.data_ptr(), ws.data_ptr(), ws.numel(),
+            _raw_stream(self._index), sync)
+        _check(code, "ckl_embed_grad")
         return dW
 
-    def _f32(self, name, t, shape):
-        if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape):
-            raise TypeError(f"{name} must be a float32 tensor of shape {tuple(shape)}")
-        self._dense(t)
-
-    def _act8(self, ckpt: Act8, cols=None):
-        self._dense(ckpt.q, ckpt.scale, ckpt.rstd)
-        if cols is not None and ckpt.q.shape[1] != cols:
-            raise ValueError(f"the checkpoint must have {cols} columns")
-        return ACT8_FORMATS[ckpt.fmt]
-
-    def _new_act8(self, T, cols, fmt, rstd):
-        return Act8(torch.empty((T, cols), dtype=torch.uint8, device=self.device),
-                    torch.empty((T, (cols + 31) // 32), dtype=torch.uint8, device=self.device), fmt,
-                    torch.empty(T, dtype=torch.float32, device=self.device) if rstd else None)
-
-    def act8_pack(self, x, fmt: str = "int8", out: Act8 | None = None, stream=None) -> Act8:
-        """The 8-bit checkpoint of x (T x cols, any cols that is a multiple of 8)."""
+    @_on_stream
+    def act8_pack(self, x, fmt: str = "int8", out: Act8 | None = None) -> Act8:
+        """The 8-bit checkpoint of x (T x cols, any cols that is a multiple of 8). With `out`, its
+        buffers and format are used."""
+        self._rows("x", x)
         if x.dim() != 2:
             raise ValueError("x must be T x cols")
-        self._rows("x", x)
-        ckpt = out if out is not None else self._new_act8(x.shape[0], x.shape[1], fmt, False)
-        f = self._act8(ckpt, x.shape[1])
-        if ckpt.q.shape[0] != x.shape[0]:
-            raise ValueError("the checkpoint must have a row for each row of x")
-        _check(lib().ckl_act8_pack(self._h, _ptr(x), x.shape[0], x.shape[1], f, _ptr(ckpt.q),
-                                   _ptr(ckpt.scale), self._stream(stream)), "ckl_act8_pack")
-        return ckpt
-
-    def act8_unpack(self, ckpt: Act8, out=None, stream=None):
-        """The values of a checkpoint (T x cols, the handle's dtype)."""
-        f = self._act8(ckpt)
+        T, cols = x.shape
         if out is None:
-            out = torch.empty(tuple(ckpt.q.shape), dtype=self.dtype, device=self.device)
-        self._rows("out", out, ckpt.q.shape)
-        _check(lib().ckl_act8_unpack(self._h, _ptr(ckpt.q), _ptr(ckpt.scale), *ckpt.q.shape, f,
-                                     _ptr(out), self._stream(stream)), "ckl_act8_unpack")
+            if fmt not in ACT8_FORMATS:
+                raise ValueError(f"fmt must be one of {sorted(ACT8_FORMATS)}")
+            out = self._new_act8(T, cols, fmt, False)
+        f = self._ckpt(out, T, cols)
+        code = self._lib.ckl_act8_pack(self._h, x.data_ptr(), T, cols, f, out.q.data_ptr(),
+                                       out.scale.data_ptr(), _raw_stream(self._index))
+        _check(code, "ckl_act8_pack")
         return out
 
+    @_on_stream
+    def act8_unpack(self, ckpt: Act8, out=None):
+        """The values of a checkpoint (T x cols, the handle's dtype)."""
+        f = self._ckpt(ckpt)
+        T, cols = ckpt.q.shape
+        if out is None:
+            out = torch.empty(T, cols, dtype=self.dtype, device=self.device)
+        else:
+            self._rows("out", out, T, cols)
+        code = self._lib.ckl_act8_unpack(self._h, ckpt.q.data_ptr(), ckpt.scale.data_ptr(), T, cols,
+                                         f, out.data_ptr(), _raw_stream(self._index))
+        _check(code, "ckl_act8_unpack")
+        return out
+
+    @_on_stream
     def act8_weight_grad(self, dY, ckpt: Act8, dW=None, accumulate: bool = False, workspace=None,
-                         sync: bool = True, stream=None):
+                         sync: bool = True):
         """dW = dY^T X' (n x cols, float32) of a linear layer Y = X W^T with X kept as the
         checkpoint; dY is T x n. dW is added to with accumulate=True."""
-        f = self._act8(ckpt)
+        f = self._ckpt(ckpt)
         T, cols = ckpt.q.shape
+        self._rows("dY", dY)
         if dY.dim() != 2 or dY.shape[0] != T:
             raise ValueError("dY must be T x n, a row for each row of the checkpoint")
-        self._rows("dY", dY)
         n = dY.shape[1]
         if dW is None:
             if accumulate:
                 raise ValueError("accumulate needs dW")
-            dW = torch.empty((n, cols), dtype=torch.float32, device=self.device)
-        self._f32("dW", dW, (n, cols))
-        ws = workspace if workspace is not None else \
-            self._workspace("ckl_act8_weight_grad_workspace_bytes", T, n, cols)
-        _check(lib().ckl_act8_weight_grad(self._h, _ptr(dY), T, n, _ptr(ckpt.q), _ptr(ckpt.scale),
-                                          cols, f, int(accumulate), _ptr(dW), _ptr(ws), ws.numel(),
-                                          self._stream(stream), int(sync)), "ckl_act8_weight_grad")
+            dW = torch.empty(n, cols, dtype=torch.float32, device=self.device)
+        else:
+            self._f32("dW", dW, n, cols)
+        ws = self._workspace("ckl_act8_weight_grad_workspace_bytes", T, n, cols) \
+            if workspace is None else self._given(workspace)
+        code = self._lib.ckl_act8_weight_grad(
+            self._h, dY.data_ptr(), T, n, ckpt.q.data_ptr(), ckpt.scale.data_ptr(), cols, f,
+            accumulate, dW.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(self._index), sync)
+        _check(code, "ckl_act8_weight_grad")
         return dW
 
+    @_on_stream
     def norm(self, x, gain, residual=None, eps: float = 1e-5, checkpoint: str | None = "int8",
-             out=None, stream=None):
+             out=None):
         """(y, s, checkpoint): s = x + residual (x itself without one), y = s / rms(s) * gain and
         the 8-bit checkpoint of s with the rows' factors, all that norm_bwd needs (None for
         checkpoint=None). out = (y, s, checkpoint): buffers to write to instead of new ones
         (s only with a residual, and it may be x's or residual's)."""
-        T = x.shape[0]
-        self._rows("x", x, (T, self.d))
-        self._rows("gain", gain, (self.d,))
+        T, d = x.shape[0], self.d
+        self._rows("x", x, T, d)
+        self._rows("gain", gain, d)
         if residual is not None:
-            self._rows("residual", residual, (T, self.d))
+            self._rows("residual", residual, T, d)
         if checkpoint is not None and checkpoint not in ACT8_FORMATS:
             raise ValueError(f"checkpoint must be None or one of {sorted(ACT8_FORMATS)}")
         if out is None:
             y = torch.empty_like(x)
-            s = torch.empty_like(x) if residual is not None else x
-            ckpt = self._new_act8(T, self.d, checkpoint, True) if checkpoint else None
+            s = x if residual is None else torch.empty_like(x)
+            ckpt = None if checkpoint is None else self._new_act8(T, d, checkpoint, True)
         else:
             y, s, ckpt = out
-            self._rows("out[0]", y, (T, self.d))
-            if residual is not None:
-                self._rows("out[1]", s, (T, self.d))
-            else:
+            self._rows("out[0]", y, T, d)
+            if residual is None:
                 s = x
+            else:
+                self._rows("out[1]", s, T, d)
             if (ckpt is None) != (checkpoint is None):
                 raise ValueError("out[2] must be an Act8 where a checkpoint is asked for")
-            if ckpt is not None and (ckpt.fmt != checkpoint or ckpt.rstd is None or
-                                     ckpt.q.shape[0] != T):
-                raise ValueError("out[2] must be a checkpoint of T rows with rstd in that format")
-        f = self._act8(ckpt, self.d) if ckpt is not None else 0
-        _check(lib().ckl_norm(self._h, _ptr(x), _ptr(residual), _ptr(gain), T, eps, f,
-                              _ptr(s) if residual is not None else None, _ptr(y),
-                              *((_ptr(ckpt.q), _ptr(ckpt.scale), _ptr(ckpt.rstd)) if ckpt is not None
-                                else (None, None, None)), self._stream(stream)), "ckl_norm")
+            if ckpt is not None and (ckpt.fmt != checkpoint or ckpt.rstd is None):
+                raise ValueError("out[2] must be a checkpoint with rstd in that format")
+        f, q, e, r = 0, None, None, None
+        if ckpt is not None:
+            f = self._ckpt(ckpt, T, d)
+            q, e, r = ckpt.q.data_ptr(), ckpt.scale.data_ptr(), ckpt.rstd.data_ptr()
+        code = self._lib.ckl_norm(
+            self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
+            gain.data_ptr(), T, eps, f, None if residual is None else s.data_ptr(), y.data_ptr(),
+            q, e, r, _raw_stream(self._index))
+        _check(code, "ckl_norm")
         return y, s, ckpt
 
+    @_on_stream
     def norm_bwd(self, dY, ckpt: Act8, gain, d_residual=None, dX=None, dgain=None,
-                 accumulate: bool = False, workspace=None, stream=None):
+                 accumulate: bool = False, workspace=None):
         """(dX, dgain) of norm from its checkpoint: dX (T x d) is the gradient of x and of
         residual, d_residual the gradient that reaches s other than through y; dgain (d,
         float32) is added to with accumulate=True."""
-        T = ckpt.q.shape[0]
-        f = self._act8(ckpt, self.d)
+        T, d = ckpt.q.shape[0], self.d
+        f = self._ckpt(ckpt, None, d)
         if ckpt.rstd is None:
             raise ValueError("the checkpoint has no rstd: it is not one of a norm")
-        self._rows("dY", dY, (T, self.d))
-        self._rows("gain", gain, (self.d,))
+        self._rows("dY", dY, T, d)
+        self._rows("gain", gain, d)
         if d_residual is not None:
-            self._rows("d_residual", d_residual, (T, self.d))
+            self._rows("d_residual", d_residual, T, d)
         if dX is None:
             dX = torch.empty_like(dY)
-        self._rows("dX", dX, (T, self.d))
+        else:
+            self._rows("dX", dX, T, d)
         if dgain is None:
             if accumulate:
                 raise ValueError("accumulate needs dgain")
-            dgain = torch.empty(self.d, dtype=torch.float32, device=self.device)
-        self._f32("dgain", dgain, (self.d,))
-        ws = workspace if workspace is not None else \
-            self._workspace("ckl_norm_bwd_workspace_bytes", T)
-        _check(lib().ckl_norm_bwd(self._h, _ptr(dY), _ptr(ckpt.q), _ptr(ckpt.scale), _ptr(ckpt.rstd),
-                                  _ptr(gain), _ptr(d_residual), T, f, int(accumulate), _ptr(dX),
-                                  _ptr(dgain), _ptr(ws), ws.numel(), self._stream(stream)),
-               "ckl_norm_bwd")
+            dgain = torch.empty(d, dtype=torch.float32, device=self.device)
+        else:
+            self._f32("dgain", dgain, d)
+        ws = self._workspace("ckl_norm_bwd_workspace_bytes", T) if workspace is None else \
+            self._given(workspace)
+        code = self._lib.ckl_norm_bwd(
+            self._h, dY.data_ptr(), ckpt.q.data_ptr(), ckpt.scale.data_ptr(), ckpt.rstd.data_ptr(),
+            gain.data_ptr(), None if d_residual is None else d_residual.data_ptr(), T, f,
+            accumulate, dX.data_ptr(), dgain.data_ptr(), ws.data_ptr(), ws.numel(),
+            _raw_stream(self._index))
+        _check(code, "ckl_norm_bwd")
         return dX, dgain
 
     def fwd_bwd_from_host(self, H_host, idx_host, logit_host, mask_host, staging, W, chunk,
