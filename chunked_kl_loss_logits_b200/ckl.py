@@ -258,18 +258,49 @@ class Act8:
         for t in (q, scale) + ((rstd,) if rstd is not None else ()):
             if not t.is_contiguous() or t.device != q.device:
                 raise ValueError("q, scale and rstd must be contiguous tensors on one device")
-        self.q, self.scale, self.fmt, self.rstd = q, scale, fmt, rstd
+        self._parts, self.fmt, self.shape, self._index = (q, scale, rstd), fmt, tuple(q.shape), \
+            q.get_device()
+        self._ptrs = (q.data_ptr(), scale.data_ptr(), None if rstd is None else rstd.data_ptr())
 
     @classmethod
-    def _of(cls, q, scale, fmt, rstd):  # parts this module made
+    def _in(cls, buf, T, cols, fmt, rstd: bool) -> "Act8":
+        """The checkpoint whose parts lie one after the other in `buf` (of _bytes() bytes): rstd,
+        then q from a multiple of 16 on, then scale."""
         self = cls.__new__(cls)
-        self.q, self.scale, self.fmt, self.rstd = q, scale, fmt, rstd
+        at, p = (4 * T + 15) // 16 * 16 if rstd else 0, buf.data_ptr()
+        self._parts, self._buf, self._at = None, buf, at
+        self.fmt, self.shape, self._index = fmt, (T, cols), buf.get_device()
+        self._ptrs = (p + at, p + at + T * cols, p if rstd else None)
         return self
+
+    @staticmethod
+    def _bytes(T, cols, rstd: bool) -> int:
+        return ((4 * T + 15) // 16 * 16 if rstd else 0) + T * (cols + (cols + 31) // 32)
+
+    def _views(self):
+        if self._parts is None:
+            (T, cols), at, b = self.shape, self._at, self._buf
+            n = T * cols
+            self._parts = (b[at:at + n].view(T, cols), b[at + n:].view(T, (cols + 31) // 32),
+                           b[:4 * T].view(torch.float32) if self._ptrs[2] is not None else None)
+        return self._parts
+
+    @property
+    def q(self):
+        return self._views()[0]
+
+    @property
+    def scale(self):
+        return self._views()[1]
+
+    @property
+    def rstd(self):
+        return self._views()[2]
 
     @property
     def nbytes(self) -> int:
-        return self.q.numel() + self.scale.numel() + \
-            (4 * self.rstd.numel() if self.rstd is not None else 0)
+        T, cols = self.shape
+        return T * (cols + (cols + 31) // 32 + (4 if self._ptrs[2] is not None else 0))
 
 
 class ChunkedKL:
@@ -552,19 +583,17 @@ class ChunkedKL:
         return mask.data_ptr()
 
     def _ckpt(self, ckpt: Act8, rows=None, cols=None) -> int:
-        T, c = ckpt.q.shape
+        T, c = ckpt.shape
         if (rows is not None and T != rows) or (cols is not None and c != cols):
             raise ValueError(f"the checkpoint must be {rows if rows is not None else T} x "
                              f"{cols if cols is not None else c}")
-        if ckpt.q.get_device() != self._index:
+        if ckpt._index != self._index:
             raise ValueError("the checkpoint must be on the handle's device")
         return ACT8_FORMATS[ckpt.fmt]
 
     def _new_act8(self, T, cols, fmt, rstd) -> Act8:
-        dev = self.device
-        return Act8._of(torch.empty(T, cols, dtype=torch.uint8, device=dev),
-                        torch.empty(T, (cols + 31) // 32, dtype=torch.uint8, device=dev), fmt,
-                        torch.empty(T, dtype=torch.float32, device=dev) if rstd else None)
+        buf = torch.empty(Act8._bytes(T, cols, rstd), dtype=torch.uint8, device=self.device)
+        return Act8._in(buf, T, cols, fmt, rstd)
 
     def _workspace(self, query, *sizes) -> torch.Tensor:
         """A workspace of the size that the library's `query` gives for these sizes."""
@@ -658,8 +687,8 @@ class ChunkedKL:
                 raise ValueError(f"fmt must be one of {sorted(ACT8_FORMATS)}")
             out = self._new_act8(T, cols, fmt, False)
         f = self._ckpt(out, T, cols)
-        code = self._lib.ckl_act8_pack(self._h, x.data_ptr(), T, cols, f, out.q.data_ptr(),
-                                       out.scale.data_ptr(), _raw_stream(self._index))
+        code = self._lib.ckl_act8_pack(self._h, x.data_ptr(), T, cols, f, *out._ptrs[:2],
+                                       _raw_stream(self._index))
         _check(code, "ckl_act8_pack")
         return out
 
@@ -667,13 +696,13 @@ class ChunkedKL:
     def act8_unpack(self, ckpt: Act8, out=None):
         """The values of a checkpoint (T x cols, the handle's dtype)."""
         f = self._ckpt(ckpt)
-        T, cols = ckpt.q.shape
+        T, cols = ckpt.shape
         if out is None:
             out = torch.empty(T, cols, dtype=self.dtype, device=self.device)
         else:
             self._rows("out", out, T, cols)
-        code = self._lib.ckl_act8_unpack(self._h, ckpt.q.data_ptr(), ckpt.scale.data_ptr(), T, cols,
-                                         f, out.data_ptr(), _raw_stream(self._index))
+        code = self._lib.ckl_act8_unpack(self._h, *ckpt._ptrs[:2], T, cols, f, out.data_ptr(),
+                                         _raw_stream(self._index))
         _check(code, "ckl_act8_unpack")
         return out
 
@@ -683,7 +712,7 @@ class ChunkedKL:
         """dW = dY^T X' (n x cols, float32) of a linear layer Y = X W^T with X kept as the
         checkpoint; dY is T x n. dW is added to with accumulate=True."""
         f = self._ckpt(ckpt)
-        T, cols = ckpt.q.shape
+        T, cols = ckpt.shape
         self._rows("dY", dY)
         if dY.dim() != 2 or dY.shape[0] != T:
             raise ValueError("dY must be T x n, a row for each row of the checkpoint")
@@ -697,8 +726,8 @@ class ChunkedKL:
         ws = self._workspace("ckl_act8_weight_grad_workspace_bytes", T, n, cols) \
             if workspace is None else self._given(workspace)
         code = self._lib.ckl_act8_weight_grad(
-            self._h, dY.data_ptr(), T, n, ckpt.q.data_ptr(), ckpt.scale.data_ptr(), cols, f,
-            accumulate, dW.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(self._index), sync)
+            self._h, dY.data_ptr(), T, n, *ckpt._ptrs[:2], cols, f, accumulate,
+            dW.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(self._index), sync)
         _check(code, "ckl_act8_weight_grad")
         return dW
 
@@ -729,16 +758,15 @@ class ChunkedKL:
                 self._rows("out[1]", s, T, d)
             if (ckpt is None) != (checkpoint is None):
                 raise ValueError("out[2] must be an Act8 where a checkpoint is asked for")
-            if ckpt is not None and (ckpt.fmt != checkpoint or ckpt.rstd is None):
+            if ckpt is not None and (ckpt.fmt != checkpoint or ckpt._ptrs[2] is None):
                 raise ValueError("out[2] must be a checkpoint with rstd in that format")
-        f, q, e, r = 0, None, None, None
+        f, kept = 0, (None, None, None)
         if ckpt is not None:
-            f = self._ckpt(ckpt, T, d)
-            q, e, r = ckpt.q.data_ptr(), ckpt.scale.data_ptr(), ckpt.rstd.data_ptr()
+            f, kept = self._ckpt(ckpt, T, d), ckpt._ptrs
         code = self._lib.ckl_norm(
             self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
             gain.data_ptr(), T, eps, f, None if residual is None else s.data_ptr(), y.data_ptr(),
-            q, e, r, _raw_stream(self._index))
+            *kept, _raw_stream(self._index))
         _check(code, "ckl_norm")
         return y, s, ckpt
 
@@ -748,9 +776,9 @@ class ChunkedKL:
         """(dX, dgain) of norm from its checkpoint: dX (T x d) is the gradient of x and of
         residual, d_residual the gradient that reaches s other than through y; dgain (d,
         float32) is added to with accumulate=True."""
-        T, d = ckpt.q.shape[0], self.d
+        T, d = ckpt.shape[0], self.d
         f = self._ckpt(ckpt, None, d)
-        if ckpt.rstd is None:
+        if ckpt._ptrs[2] is None:
             raise ValueError("the checkpoint has no rstd: it is not one of a norm")
         self._rows("dY", dY, T, d)
         self._rows("gain", gain, d)
@@ -769,10 +797,9 @@ class ChunkedKL:
         ws = self._workspace("ckl_norm_bwd_workspace_bytes", T) if workspace is None else \
             self._given(workspace)
         code = self._lib.ckl_norm_bwd(
-            self._h, dY.data_ptr(), ckpt.q.data_ptr(), ckpt.scale.data_ptr(), ckpt.rstd.data_ptr(),
-            gain.data_ptr(), None if d_residual is None else d_residual.data_ptr(), T, f,
-            accumulate, dX.data_ptr(), dgain.data_ptr(), ws.data_ptr(), ws.numel(),
-            _raw_stream(self._index))
+            self._h, dY.data_ptr(), *ckpt._ptrs, gain.data_ptr(),
+            None if d_residual is None else d_residual.data_ptr(), T, f, accumulate, dX.data_ptr(),
+            dgain.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(self._index))
         _check(code, "ckl_norm_bwd")
         return dX, dgain
 
@@ -933,7 +960,8 @@ class _RmsNormFn(torch.autograd.Function):
         flat = x.detach().view(-1, handle.d)
         res = None if residual is None else residual.detach().view(-1, handle.d)
         y, s, ckpt = handle.norm(flat, gain.detach(), res, eps, fmt)
-        ctx.save_for_backward(ckpt.q, ckpt.scale, ckpt.rstd, gain)
+        ctx.save_for_backward(ckpt._buf, gain)
+        ctx.rows = flat.shape[0]
         ctx.fmt, ctx.handle, ctx.has_residual = fmt, handle, residual is not None
         ctx.set_materialize_grads(False)
         return y.view(x.shape) if residual is None else (y.view(x.shape), s.view(x.shape))
@@ -941,12 +969,13 @@ class _RmsNormFn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dY, d_sum=None):
-        q, scale, rstd, gain = ctx.saved_tensors
+        buf, gain = ctx.saved_tensors
         if dY is None:  # only s was used
             return d_sum, None, d_sum if ctx.has_residual else None, None, None, None
         h = ctx.handle
         flat = [None if g is None else g.contiguous().view(-1, h.d) for g in (dY, d_sum)]
-        dX, dgain = h.norm_bwd(flat[0], Act8(q, scale, ctx.fmt, rstd), gain.detach(), flat[1])
+        ckpt = Act8._in(buf, ctx.rows, h.d, ctx.fmt, True)
+        dX, dgain = h.norm_bwd(flat[0], ckpt, gain.detach(), flat[1])
         dX = dX.view(dY.shape)
         return dX, dgain.to(gain.dtype), dX if ctx.has_residual else None, None, None, None
 

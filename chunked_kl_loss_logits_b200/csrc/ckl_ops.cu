@@ -39,18 +39,18 @@ EmbedIds ids_of(const ckl_ctx* h, const int32_t* ids, const uint8_t* mask, int64
 }
 
 struct EmbedGradPlan {
-  int tile = 0;
+  EmbedShape shape{};
   size_t off_a = 0, off_b = 0, off_part = 0, total = 0;
 };
 
 EmbedGradPlan embed_grad_plan(const ckl_ctx* h, int64_t T) {
   EmbedGradPlan p;
-  p.tile = embed_tile(T, (int)h->d, h->num_sms);
+  p.shape = embed_shape(T, (int)h->d, h->num_sms);
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
   p.off_a = take((size_t)T * 8);
   p.off_b = take((size_t)T * 8);
-  p.off_part = take((size_t)((T + p.tile - 1) / p.tile) * 2 * h->d * 4);
+  p.off_part = take((size_t)((T + p.shape.tile() - 1) / p.shape.tile()) * 2 * h->d * 4);
   p.total = o;
   return p;
 }
@@ -255,23 +255,25 @@ ckl_status ckl_embed_grad(ckl_handle h, const int32_t* ids, const uint8_t* mask,
   cudaError_t err = cudaSuccess;
   auto chk = [&](cudaError_t e) { if (e != cudaSuccess && err == cudaSuccess) err = e; };
   const int d = (int)h->d, V = (int)h->V;
-  if (!accumulate) chk(cudaMemsetAsync(dW, 0, (size_t)V * d * 4, s));
-  if (T > 0) {
+  if (T == 0) {
+    if (!accumulate) chk(cudaMemsetAsync(dW, 0, (size_t)V * d * 4, s));
+  } else {
     unsigned char* base = static_cast<unsigned char*>(workspace);
     uint64_t* a = reinterpret_cast<uint64_t*>(base + P.off_a);
     uint64_t* b = reinterpret_cast<uint64_t*>(base + P.off_b);
     float* part = reinterpret_cast<float*>(base + P.off_part);
     const uint64_t* sorted = embed_sort_result(V) ? b : a;
     Launcher L{h, s};
-    chk(L(KID_EMBED_SORT, 0, (double)T * 12, [&] {
-      chk(launch_embed_sort(ids_of(h, ids, mask, T, V_total, v0), a, b, s));
+    const int64_t n_fill = accumulate ? 0 : (int64_t)V * d;
+    chk(L(KID_EMBED_SORT, 0, (double)T * 12 + 4.0 * n_fill, [&] {
+      chk(launch_embed_sort(ids_of(h, ids, mask, T, V_total, v0), a, b, dW, n_fill, h->num_sms, s));
     }));
     chk(L(KID_EMBED_GRAD, 0, (double)T * d * elem(h), [&] {
-      launch_embed_grad(sorted, T, V, h->dtype == CKL_BF16, dX, d, P.tile, scale, accumulate != 0,
+      launch_embed_grad(sorted, T, V, h->dtype == CKL_BF16, dX, d, P.shape, scale, accumulate != 0,
                         dW, part, s);
     }));
     chk(L(KID_EMBED_JOIN, 0, 0, [&] {
-      launch_embed_join(sorted, T, V, d, P.tile, scale, accumulate != 0, dW, part, s);
+      launch_embed_join(sorted, T, V, d, P.shape, scale, accumulate != 0, dW, part, s);
     }));
   }
   if ((st = cuda_status(err)) != CKL_OK) return st;
@@ -335,14 +337,16 @@ ckl_status ckl_norm(ckl_handle h, const void* X, const void* residual, const voi
   a.sum = sum; a.y = Y; a.q = static_cast<uint8_t*>(q); a.e = scale; a.rstd = rstd;
   Launcher L{h, s};
   const double per = elem(h) * (residual ? 4.0 : 2.0) + (q ? 33.0 / 32 : 0.0);
-  return cuda_status(L(KID_NORM_FWD, 0, (double)T * h->d * per, [&] {
-    launch_norm_fwd(a, h->dtype == CKL_BF16, s);
-  }));
+  cudaError_t set = cudaSuccess;
+  const cudaError_t err = L(KID_NORM_FWD, 0, (double)T * h->d * per, [&] {
+    set = launch_norm_fwd(a, h->dtype == CKL_BF16, h->num_sms, s);
+  });
+  return cuda_status(err != cudaSuccess ? err : set);
 }
 
 ckl_status ckl_norm_bwd_workspace_bytes(ckl_handle h, int64_t T, size_t* bytes) {
   if (!h || !bytes || T < 0) return CKL_ERR_INVALID_ARG;
-  *bytes = (size_t)norm_part_rows(T, (int)h->d, h->num_sms) * h->d * 4;
+  *bytes = (size_t)norm_part_rows(T, (int)h->d, h->dtype == CKL_BF16, h->num_sms) * h->d * 4;
   return CKL_OK;
 }
 
@@ -357,7 +361,7 @@ ckl_status ckl_norm_bwd(ckl_handle h, const void* dY, const void* q, const uint8
     if (p && !aligned(p, 16)) return CKL_ERR_ALIGNMENT;
   if (!aligned(dgain, 4) || (rstd && !aligned(rstd, 4))) return CKL_ERR_ALIGNMENT;
   const int d = (int)h->d;
-  const int64_t rows = norm_part_rows(T, d, h->num_sms);
+  const int64_t rows = norm_part_rows(T, d, h->dtype == CKL_BF16, h->num_sms);
   if (T > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)rows * d * 4))
     return CKL_ERR_WORKSPACE;
   DeviceGuard guard(h->device);
@@ -373,8 +377,10 @@ ckl_status ckl_norm_bwd(ckl_handle h, const void* dY, const void* q, const uint8
   a.part = static_cast<float*>(workspace);
   Launcher L{h, s};
   const double per = elem(h) * (d_sum ? 3.0 : 2.0) + 33.0 / 32;
+  cudaError_t set = cudaSuccess;
   cudaError_t err = L(KID_NORM_BWD, 0, (double)T * d * per,
-                      [&] { launch_norm_bwd(a, h->dtype == CKL_BF16, h->num_sms, s); });
+                      [&] { set = launch_norm_bwd(a, h->dtype == CKL_BF16, h->num_sms, s); });
+  if (err == cudaSuccess) err = set;
   if (err == cudaSuccess)
     err = L(KID_NORM_DGAIN, 0, (double)rows * d * 4,
             [&] { launch_norm_dgain(a.part, rows, d, accumulate != 0, dgain, s); });

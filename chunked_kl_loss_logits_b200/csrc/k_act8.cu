@@ -9,9 +9,9 @@
 //             (dX is the gradient of x and of r; dS the gradient that reaches s from
 //             elsewhere, as s is the residual stream that the next layer adds to)
 // Everything is held in fp32 between the loads and the one rounding of each output.
-// All of these are bound by memory. A row is read once, kept in registers (16-byte loads,
-// one vector of eight columns a lane, four lanes to an 8-bit block) while its sum goes
-// round the warps that share it, and written from there.
+// All of these are bound by memory. A row is read once, kept in registers (one vector of
+// eight columns a lane, four lanes to an 8-bit block) while its sum goes round the warps that
+// share it, and written from there.
 #include "common.cuh"
 #include "k_ops.h"
 #include "ops.cuh"
@@ -81,162 +81,222 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Sum over the WPR warps of a row (all threads of the block call it; each row group r of the
-// block has its own line of `red`).
+// The norm kernels: a block of WPR warps walks rows in steps of the grid, each lane with VPT
+// vectors of eight columns. What it needs of the rows ahead is on its way to shared memory
+// (cp.async, each thread its own vectors, so that nothing but the row sum is synchronised).
+template <typename T, int WPR, int VPT, bool BWD>
+struct NormCfg {
+  static constexpr int kThreads = WPR * 32;
+  // blocks per SM: 24 warps' worth backward (the sums of dg are in registers), 36 forward
+  static constexpr int kWant = (BWD ? 24 : 36) / WPR;
+  static constexpr int kPerSm = kWant < 1 ? 1 : kWant > 16 ? 16 : kWant;
+  static constexpr size_t kStage = (size_t)kThreads * VPT * (2 * sizeof(Raw8<T>) + (BWD ? 8 : 0));
+  static constexpr size_t kRoom = 200 * 1024 / kPerSm;
+  static constexpr int kDepth = kRoom / kStage >= 4 ? 4 : kRoom / kStage >= 2 ? 2 : 1;
+  static constexpr size_t kSmem = kStage * kDepth;
+  static_assert(kSmem <= 200 * 1024, "shared memory per block");
+};
+
+// Sum over the WPR warps of a row (all threads of the block call it, `red` in turn).
 template <int WPR>
-__device__ __forceinline__ float row_add(float v, float (*red)[32], int r, int lw, int lane) {
+__device__ __forceinline__ float row_add(float v, float* red, int warp, int lane) {
   v = warp_add(v);
   if (WPR == 1) return v;
-  if (lane == 0) red[r][lw] = v;
+  if (lane == 0) red[warp] = v;
   __syncthreads();
-  float t = red[r][0];
+  float t = red[0];
 #pragma unroll
-  for (int w = 1; w < WPR; ++w) t += red[r][w];
+  for (int w = 1; w < WPR; ++w) t += red[w];
   return t;
 }
 
-// WPR warps share a row, each lane holding VPT vectors of eight columns. Blocks of eight
-// warps (8 / WPR rows), or of one row where it takes 32 warps.
-template <int WPR>
-constexpr int kNormThreads = WPR > 8 ? WPR * 32 : 256;
-
 template <typename T, int WPR, int VPT>
-__global__ void __launch_bounds__(kNormThreads<WPR>) norm_fwd_kernel(const NormArgs a) {
-  constexpr int R = kNormThreads<WPR> / 32 / WPR;
-  __shared__ float red[R][32];
+__global__ void __launch_bounds__(WPR * 32, NormCfg<T, WPR, VPT, false>::kPerSm)
+    norm_fwd_kernel(const NormArgs a) {
+  using C = NormCfg<T, WPR, VPT, false>;
+  constexpr int D = C::kDepth;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float red[2][WPR];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = warp / WPR, lw = warp % WPR;
-  const int64_t t = (int64_t)blockIdx.x * R + r;
   const int nvec = a.d / 8, nb = (nvec + 3) / 4;
-  const bool row_ok = t < a.T;
-  const T* x = (const T*)a.x + t * a.d;
-  const T* res = (const T*)a.res + t * a.d;
-  Raw8<T> s[VPT];
-  float ss = 0.f;
+  Raw8<T>* xs = reinterpret_cast<Raw8<T>*>(smem) + threadIdx.x;  // [stage][x, res][i] of this thread
+  auto slot = [&](int stage, int which, int i) {
+    return xs + ((stage * 2 + which) * VPT + i) * C::kThreads;
+  };
+  auto vec = [&](int i) { return (i * WPR + warp) * 32 + lane; };
+  auto fetch = [&](int64_t t, int stage) {
+    if (t < a.T) {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = (i * WPR + lw) * 32 + lane;
-    s[i] = row_ok && v < nvec ? load8(x + v * 8) : zero8<T>();
-    if (a.res && row_ok && v < nvec) {
-      float f[8], g[8];
-      to_f32(s[i], f);
-      to_f32(load8(res + v * 8), g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += g[j];
-      s[i] = from_f32<T>(f);
-    }
-    float f[8];
-    to_f32(s[i], f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
-  }
-  ss = row_add<WPR>(ss, red, r, lw, lane);
-  const float rstd = 1.f / sqrtf(ss / (float)a.d + a.eps);
-  if (a.rstd && row_ok && lw == 0 && lane == 0) a.rstd[t] = rstd;
-  T* sum = (T*)a.sum + t * a.d;
-  T* y = (T*)a.y + t * a.d;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = (i * WPR + lw) * 32 + lane;
-    const bool ok = row_ok && v < nvec;
-    float f[8];
-    to_f32(s[i], f);
-    if (a.q) {
-      const uint32_t byte = act8_scale_byte(quad_max(amax_bits8(f)), a.fmt);
-      if (ok) {
-        *reinterpret_cast<uint2*>(a.q + t * a.d + v * 8) = act8_encode(f, byte, a.fmt);
-        if ((lane & 3) == 0) a.e[t * nb + (v >> 2)] = (uint8_t)byte;
+      for (int i = 0; i < VPT; ++i) {
+        if (vec(i) >= nvec) break;
+        copy8(slot(stage, 0, i), (const T*)a.x + t * a.d + vec(i) * 8);
+        if (a.res) copy8(slot(stage, 1, i), (const T*)a.res + t * a.d + vec(i) * 8);
       }
     }
-    if (!ok) continue;
-    if (a.res) store8(sum + v * 8, s[i]);
-    float g[8];
-    to_f32(load8((const T*)a.gain + v * 8), g);
+    cp_async_commit();
+  };
+  const int64_t step = gridDim.x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * g[j];
-    store8(y + v * 8, from_f32<T>(f));
+  for (int u = 0; u < D; ++u) fetch(blockIdx.x + u * step, u);
+  Raw8<T> g[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    g[i] = vec(i) < nvec ? load8((const T*)a.gain + vec(i) * 8) : zero8<T>();
+  int stage = 0, flip = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += step, flip ^= 1) {
+    cp_async_wait<D - 1>();
+    Raw8<T> s[VPT];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const bool ok = vec(i) < nvec;
+      s[i] = ok ? *slot(stage, 0, i) : zero8<T>();
+      float f[8];
+      to_f32(s[i], f);
+      if (a.res && ok) {
+        float p[8];
+        to_f32(*slot(stage, 1, i), p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] += p[j];
+        s[i] = from_f32<T>(f);
+        to_f32(s[i], f);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+    }
+    fetch(t + D * step, stage);
+    if (++stage == D) stage = 0;
+    ss = row_add<WPR>(ss, red[flip], warp, lane);
+    const float rstd = 1.f / sqrtf(ss / (float)a.d + a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const bool ok = vec(i) < nvec;
+      float f[8];
+      to_f32(s[i], f);
+      if (a.q) {
+        const uint32_t byte = act8_scale_byte(quad_max(amax_bits8(f)), a.fmt);
+        if (ok) {
+          *reinterpret_cast<uint2*>(a.q + t * a.d + vec(i) * 8) = act8_encode(f, byte, a.fmt);
+          if ((lane & 3) == 0) a.e[t * nb + (vec(i) >> 2)] = (uint8_t)byte;
+        }
+      }
+      if (!ok) continue;
+      if (a.res) store8((T*)a.sum + t * a.d + vec(i) * 8, s[i]);
+      float w[8];
+      to_f32(g[i], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * w[j];
+      store8((T*)a.y + t * a.d + vec(i) * 8, from_f32<T>(f));
+    }
   }
+  cp_async_wait<0>();
 }
 
-// A block walks rows in steps of the grid and keeps its columns' share of dg in registers;
-// each row group leaves one line of partial sums, added up by norm_dgain_kernel.
+// Keeps its columns' share of dg in registers and leaves it as one line of partial sums, added
+// up by norm_dgain_kernel.
 template <typename T, int WPR, int VPT>
-__global__ void __launch_bounds__(kNormThreads<WPR>) norm_bwd_kernel(const NormArgs a) {
-  constexpr int R = kNormThreads<WPR> / 32 / WPR;
-  __shared__ float red[2][R][32];
+__global__ void __launch_bounds__(WPR * 32, NormCfg<T, WPR, VPT, true>::kPerSm)
+    norm_bwd_kernel(const NormArgs a) {
+  using C = NormCfg<T, WPR, VPT, true>;
+  constexpr int D = C::kDepth;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float red[2][WPR];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = warp / WPR, lw = warp % WPR;
   const int nvec = a.d / 8, nb = (nvec + 3) / 4;
   const float inv_d = 1.f / (float)a.d;
+  Raw8<T>* xs = reinterpret_cast<Raw8<T>*>(smem) + threadIdx.x;  // [stage][dY, dS][i]
+  uint2* qs = reinterpret_cast<uint2*>(smem + (size_t)D * 2 * VPT * C::kThreads * sizeof(Raw8<T>)) +
+              threadIdx.x;                                       // [stage][i]
+  auto slot = [&](int stage, int which, int i) {
+    return xs + ((stage * 2 + which) * VPT + i) * C::kThreads;
+  };
+  auto qslot = [&](int stage, int i) { return qs + (stage * VPT + i) * C::kThreads; };
+  auto vec = [&](int i) { return (i * WPR + warp) * 32 + lane; };
+  auto fetch = [&](int64_t t, int stage) {
+    if (t < a.T) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        if (vec(i) >= nvec) break;
+        copy8(slot(stage, 0, i), (const T*)a.x + t * a.d + vec(i) * 8);
+        cp_async<8>(qslot(stage, i), a.q + t * a.d + vec(i) * 8);
+        if (a.res) copy8(slot(stage, 1, i), (const T*)a.res + t * a.d + vec(i) * 8);
+      }
+      // scales and factors are loaded one row ahead, from L2
+      if (lane == 0) prefetch_l2(a.e + t * nb + min(warp * 32 / 4, nb - 1));
+      if (threadIdx.x == 0) prefetch_l2(a.rstd + t);
+    }
+    cp_async_commit();
+  };
+  const int64_t step = gridDim.x;
+#pragma unroll
+  for (int u = 0; u < D; ++u) fetch(blockIdx.x + u * step, u);
   Raw8<T> g[VPT];
   float dg[VPT][8];
+  uint32_t e[VPT];
+  float rstd = a.rstd[blockIdx.x];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int v = (i * WPR + lw) * 32 + lane;
-    g[i] = v < nvec ? load8((const T*)a.gain + v * 8) : zero8<T>();
+    g[i] = vec(i) < nvec ? load8((const T*)a.gain + vec(i) * 8) : zero8<T>();
+    e[i] = vec(i) < nvec ? a.e[(int64_t)blockIdx.x * nb + (vec(i) >> 2)] : 1u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = 0.f;
   }
-  int flip = 0;
-  for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < a.T; t0 += (int64_t)gridDim.x * R, flip ^= 1) {
-    const int64_t t = t0 + r;
-    const bool row_ok = t < a.T;
-    const float rstd = row_ok ? a.rstd[t] : 0.f;
-    Raw8<T> dy[VPT];
-    uint2 q[VPT];
-    uint32_t e[VPT];
+  int stage = 0, flip = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += step, flip ^= 1) {
+    const bool more = t + step < a.T;
+    const float next_rstd = more ? a.rstd[t + step] : 0.f;
+    uint32_t next_e[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = (i * WPR + lw) * 32 + lane;
-      dy[i] = zero8<T>();
-      q[i] = make_uint2(0u, 0u);
-      e[i] = 1u;
-      if (row_ok && v < nvec) {
-        dy[i] = load8((const T*)a.x + t * a.d + v * 8);
-        q[i] = *reinterpret_cast<const uint2*>(a.q + t * a.d + v * 8);
-        e[i] = a.e[t * nb + (v >> 2)];
-      }
-    }
+    for (int i = 0; i < VPT; ++i)
+      next_e[i] = more && vec(i) < nvec ? a.e[(t + step) * nb + (vec(i) >> 2)] : 1u;
+    cp_async_wait<D - 1>();
+    Raw8<T> dy[VPT];
+    float h[VPT][8];
     float c = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      float h[8], d[8], w[8];
-      act8_decode(q[i], act8_scale(e[i]), a.fmt, h);
+      const bool ok = vec(i) < nvec;
+      dy[i] = ok ? *slot(stage, 0, i) : zero8<T>();
+      act8_decode(ok ? *qslot(stage, i) : make_uint2(0u, 0u), act8_scale(e[i]), a.fmt, h[i]);
+      float d[8], w[8];
       to_f32(dy[i], d);
       to_f32(g[i], w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float dh = d[j] * (h[j] * rstd);
+        h[i][j] *= rstd;
+        const float dh = d[j] * h[i][j];
         dg[i][j] += dh;
         c = fmaf(dh, w[j], c);
       }
     }
-    c = row_add<WPR>(c, red[flip], r, lw, lane) * inv_d;
+    c = row_add<WPR>(c, red[flip], warp, lane) * inv_d;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = (i * WPR + lw) * 32 + lane;
-      if (!row_ok || v >= nvec) continue;
-      float h[8], d[8], w[8];
-      act8_decode(q[i], act8_scale(e[i]), a.fmt, h);
+      if (vec(i) >= nvec) continue;
+      float d[8], w[8];
       to_f32(dy[i], d);
       to_f32(g[i], w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = rstd * (d[j] * w[j] - h[j] * rstd * c);
+      for (int j = 0; j < 8; ++j) d[j] = rstd * (d[j] * w[j] - h[i][j] * c);
       if (a.res) {
         float p[8];
-        to_f32(load8((const T*)a.res + t * a.d + v * 8), p);
+        to_f32(*slot(stage, 1, i), p);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] += p[j];
       }
-      store8((T*)a.y + t * a.d + v * 8, from_f32<T>(d));
+      store8((T*)a.y + t * a.d + vec(i) * 8, from_f32<T>(d));
     }
-  }
-  float* out = a.part + ((int64_t)blockIdx.x * R + r) * a.d;
+    fetch(t + D * step, stage);
+    if (++stage == D) stage = 0;
+    rstd = next_rstd;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = (i * WPR + lw) * 32 + lane;
-    if (v < nvec) store8(out + v * 8, from_f32<float>(dg[i]));
+    for (int i = 0; i < VPT; ++i) e[i] = next_e[i];
   }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    if (vec(i) < nvec) store8(a.part + (int64_t)blockIdx.x * a.d + vec(i) * 8, from_f32<float>(dg[i]));
 }
 
 // 32 columns per block; each of 32 warps adds every 32nd line, then the warps' sums in order.
@@ -259,43 +319,65 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// Warps per row: the fewest whose lanes hold the row in at most four vectors each; rows of
-// more than 1024 vectors take a block of 32 warps (handles have at most 3200 vectors).
-int warps_per_row(int nvec) {
-  for (int w = 1; w <= 8; w *= 2)
-    if (nvec <= w * 128) return w;
-  return 32;
-}
-
-template <typename F>
+// Warps per row and vectors per lane: one vector a lane up to 16 warps (4096 columns), then as
+// many vectors as it takes (handles have at most 3200, in fp32 1600).
+template <typename T, typename F>
 void pick_norm(int nvec, F&& f) {  // f(integral_constant WPR, integral_constant VPT)
-  const int wpr = warps_per_row(nvec), vpt = (nvec + wpr * 32 - 1) / (wpr * 32);
-  auto with = [&](auto w) {
-    switch (vpt) {
-      case 1: f(w, std::integral_constant<int, 1>{}); break;
-      case 2: f(w, std::integral_constant<int, 2>{}); break;
-      case 3: f(w, std::integral_constant<int, 3>{}); break;
-      default: f(w, std::integral_constant<int, 4>{}); break;
-    }
-  };
-  switch (wpr) {
-    case 1: with(std::integral_constant<int, 1>{}); break;
-    case 2: with(std::integral_constant<int, 2>{}); break;
-    case 4: with(std::integral_constant<int, 4>{}); break;
-    case 8: with(std::integral_constant<int, 8>{}); break;
-    default: with(std::integral_constant<int, 32>{}); break;
-  }
+#define CKL_NORM_CASE(W, V)          \
+  if (nvec <= W * 32 * V)            \
+    return f(std::integral_constant<int, W>{}, std::integral_constant<int, V>{});
+  CKL_NORM_CASE(1, 1)
+  CKL_NORM_CASE(2, 1)
+  CKL_NORM_CASE(3, 1)
+  CKL_NORM_CASE(4, 1)
+  CKL_NORM_CASE(6, 1)
+  CKL_NORM_CASE(8, 1)
+  CKL_NORM_CASE(12, 1)
+  CKL_NORM_CASE(16, 1)
+  CKL_NORM_CASE(16, 2)
+  CKL_NORM_CASE(16, 4)
+  if constexpr (sizeof(T) == 2) f(std::integral_constant<int, 16>{}, std::integral_constant<int, 7>{});
+#undef CKL_NORM_CASE
 }
 
-int rows_per_block(int nvec) {
-  const int w = warps_per_row(nvec);
-  return w > 8 ? 1 : 8 / w;
+template <typename T, bool BWD>
+int64_t norm_blocks(int64_t T_, int d, int num_sms) {
+  int per_sm = 1;
+  pick_norm<T>(d / 8, [&](auto w, auto v) {
+    per_sm = NormCfg<T, decltype(w)::value, decltype(v)::value, BWD>::kPerSm;
+  });
+  const int64_t most = (int64_t)num_sms * per_sm;
+  return T_ < most ? T_ : most;
 }
 
-int64_t norm_bwd_blocks(int64_t T, int d, int num_sms) {
-  const int R = rows_per_block(d / 8);
-  const int64_t need = (T + R - 1) / R, most = (int64_t)num_sms * 4;
-  return need < most ? need : most;
+template <typename T>
+cudaError_t norm_fwd(const NormArgs& a, int num_sms, cudaStream_t s) {
+  const unsigned blocks = (unsigned)norm_blocks<T, false>(a.T, a.d, num_sms);
+  cudaError_t err = cudaErrorInvalidValue;
+  pick_norm<T>(a.d / 8, [&](auto w, auto v) {
+    constexpr int WPR = decltype(w)::value, VPT = decltype(v)::value;
+    using C = NormCfg<T, WPR, VPT, false>;
+    static std::atomic<uint64_t> attr_set{0};
+    err = smem_once(norm_fwd_kernel<T, WPR, VPT>, C::kSmem, attr_set);
+    if (err == cudaSuccess)
+      norm_fwd_kernel<T, WPR, VPT><<<blocks, C::kThreads, C::kSmem, s>>>(a);
+  });
+  return err;
+}
+
+template <typename T>
+cudaError_t norm_bwd(const NormArgs& a, int num_sms, cudaStream_t s) {
+  const unsigned blocks = (unsigned)norm_blocks<T, true>(a.T, a.d, num_sms);
+  cudaError_t err = cudaErrorInvalidValue;
+  pick_norm<T>(a.d / 8, [&](auto w, auto v) {
+    constexpr int WPR = decltype(w)::value, VPT = decltype(v)::value;
+    using C = NormCfg<T, WPR, VPT, true>;
+    static std::atomic<uint64_t> attr_set{0};
+    err = smem_once(norm_bwd_kernel<T, WPR, VPT>, C::kSmem, attr_set);
+    if (err == cudaSuccess)
+      norm_bwd_kernel<T, WPR, VPT><<<blocks, C::kThreads, C::kSmem, s>>>(a);
+  });
+  return err;
 }
 
 }  // namespace
@@ -320,27 +402,16 @@ void launch_act8_unpack(bool bf16, const uint8_t* q, const uint8_t* e, int64_t T
     act8_unpack_kernel<float><<<blocks, 256, 0, s>>>(q, e, T, nvec, slabs, fmt, (float*)out);
 }
 
-void launch_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t s) {
-  const int R = rows_per_block(a.d / 8);
-  const unsigned blocks = (unsigned)((a.T + R - 1) / R);
-  pick_norm(a.d / 8, [&](auto w, auto v) {
-    constexpr int WPR = decltype(w)::value, VPT = decltype(v)::value;
-    if (bf16) norm_fwd_kernel<uint16_t, WPR, VPT><<<blocks, kNormThreads<WPR>, 0, s>>>(a);
-    else norm_fwd_kernel<float, WPR, VPT><<<blocks, kNormThreads<WPR>, 0, s>>>(a);
-  });
+cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s) {
+  return bf16 ? norm_fwd<uint16_t>(a, num_sms, s) : norm_fwd<float>(a, num_sms, s);
 }
 
-int64_t norm_part_rows(int64_t T, int d, int num_sms) {
-  return norm_bwd_blocks(T, d, num_sms) * rows_per_block(d / 8);
+int64_t norm_part_rows(int64_t T, int d, bool bf16, int num_sms) {
+  return bf16 ? norm_blocks<uint16_t, true>(T, d, num_sms) : norm_blocks<float, true>(T, d, num_sms);
 }
 
-void launch_norm_bwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s) {
-  const unsigned blocks = (unsigned)norm_bwd_blocks(a.T, a.d, num_sms);
-  pick_norm(a.d / 8, [&](auto w, auto v) {
-    constexpr int WPR = decltype(w)::value, VPT = decltype(v)::value;
-    if (bf16) norm_bwd_kernel<uint16_t, WPR, VPT><<<blocks, kNormThreads<WPR>, 0, s>>>(a);
-    else norm_bwd_kernel<float, WPR, VPT><<<blocks, kNormThreads<WPR>, 0, s>>>(a);
-  });
+cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s) {
+  return bf16 ? norm_bwd<uint16_t>(a, num_sms, s) : norm_bwd<float>(a, num_sms, s);
 }
 
 void launch_norm_dgain(const float* part, int64_t rows, int d, bool accumulate, float* out,

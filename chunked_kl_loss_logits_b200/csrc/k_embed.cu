@@ -8,8 +8,10 @@
 // forward moves a row in and a row out per token; the gradient reads dX once and reads and
 // writes the rows of the ids that occur. Atomic adds would read and write dW once per
 // token and make the sums' order, hence their last bits, change from run to run; instead
-// the tokens are sorted by (id, position) and each thread walks `tile` neighbouring sorted
-// tokens with eight columns of the running row sum in registers.
+// the tokens are sorted by (id, position) and each thread walks neighbouring sorted tokens
+// with eight columns of the running row sum in registers.
+#include <algorithm>
+
 #include "common.cuh"
 #include "k_ops.h"
 #include "ops.cuh"
@@ -70,6 +72,7 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedIds a, const T* _
 // digits, then over warps" gives every item its place, and equal keys keep their order.
 // The digit counts of the other CTAs are read from their shared memory.
 constexpr int kSortWarps = 32;
+constexpr int kBatch = 8;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxBins = 1 << kMaxDigitBits;
 constexpr size_t kSortSmem = (size_t)(kSortWarps * kMaxBins + 2 * kMaxBins + 32) * 4;
@@ -80,15 +83,22 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
+// The first cluster sorts. The others (where dW is to be overwritten) zero dW meanwhile.
 __global__ void __launch_bounds__(kSortWarps * 32, 1)
     embed_sort_kernel(const EmbedIds a, int n_pass, int bits, int cluster, uint64_t* buf_a,
-                      uint64_t* buf_b) {
+                      uint64_t* buf_b, float4* fill, int64_t n_fill) {
   extern __shared__ uint32_t sm[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (blockIdx.x >= cluster) {
+    const int64_t step = (int64_t)(gridDim.x - cluster) * blockDim.x;
+    for (int64_t i = (int64_t)(blockIdx.x - cluster) * blockDim.x + tid; i < n_fill; i += step)
+      fill[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    return;
+  }
   uint32_t* hist = sm;                          // [warp][bin] counts, then places
   uint32_t* tot = sm + kSortWarps * kMaxBins;   // [bin] this CTA's counts (read by the others)
   uint32_t* base = tot + kMaxBins;              // [bin] first place of this CTA's items
   uint32_t* wsum = base + kMaxBins;             // [32]
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_ctarank();
   const int bins = 1 << bits;
   const int64_t per = ((a.T + (int64_t)cluster * kSortWarps * 32 - 1) /
@@ -102,17 +112,31 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
     const uint64_t* in = (p & 1) ? buf_a : buf_b;  // pass 0 reads the ids
     uint64_t* out = (p & 1) ? buf_b : buf_a;
     const int shift = 32 + p * bits;
-    auto item = [&](int64_t i) -> uint64_t {
-      if (p == 0) return (uint64_t)(uint32_t)token_row(a, i, bad) << 32 | (uint64_t)i;
-      return __ldcg(reinterpret_cast<const unsigned long long*>(in) + i);
+    // kBatch items a lane at a time; a warp's range of at most one batch stays in registers
+    uint64_t it[kBatch];
+    auto load = [&](int64_t ib) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t i = ib + j * 32 + lane;
+        if (i >= i1) continue;
+        it[j] = p == 0 ? (uint64_t)(uint32_t)token_row(a, i, bad) << 32 | (uint64_t)i
+                       : __ldcg(reinterpret_cast<const unsigned long long*>(in) + i);
+      }
     };
+    auto digit = [&](uint64_t v) { return (uint32_t)(v >> shift) & (uint32_t)(bins - 1); };
+    if (i0 < i1) load(i0);
     for (int b = lane; b < bins; b += 32) myhist[b] = 0;
     __syncwarp();
-    for (int64_t i = i0 + lane; i < i1; i += 32)
-      atomicAdd(&myhist[(uint32_t)(item(i) >> shift) & (bins - 1)], 1u);
+    for (int64_t ib = i0; ib < i1; ib += kBatch * 32) {
+      if (ib > i0) load(ib);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (ib + j * 32 + lane < i1) atomicAdd(&myhist[digit(it[j])], 1u);
+    }
     __syncthreads();
     uint32_t mine = 0;
     if (tid < bins) {
+#pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t c = hist[w * bins + tid];
         hist[w * bins + tid] = mine;
@@ -123,6 +147,7 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
     cluster_sync();
     uint32_t before = 0, all = 0;
     if (tid < bins) {
+#pragma unroll 8
       for (int r = 0; r < cluster; ++r) {
         const uint32_t c = ld_cluster_u32(cluster_map(tot + tid, (uint32_t)r));
         if (r < rank) before += c;
@@ -144,19 +169,23 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
       base[tid] = pre + incl - all + before;
     }
     __syncthreads();
-    for (int64_t ib = i0; ib < i1; ib += 32) {
-      const int64_t i = ib + lane;
-      const unsigned act = __ballot_sync(0xffffffffu, i < i1);
-      if (i < i1) {
-        const uint64_t it = item(i);
-        const uint32_t dg = (uint32_t)(it >> shift) & (bins - 1);
-        const unsigned same = __match_any_sync(act, dg);
-        const uint32_t at = myhist[dg];
-        __syncwarp(act);
-        if (lane == __ffs(same) - 1) myhist[dg] = at + __popc(same);
-        out[base[dg] + at + __popc(same & ((1u << lane) - 1))] = it;
+    for (int64_t ib = i0; ib < i1; ib += kBatch * 32) {
+      if (i1 - i0 > kBatch * 32) load(ib);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (ib + j * 32 >= i1) break;
+        const bool have = ib + j * 32 + lane < i1;
+        const unsigned act = __ballot_sync(0xffffffffu, have);
+        if (have) {
+          const uint32_t dg = digit(it[j]);
+          const unsigned same = __match_any_sync(act, dg);
+          const uint32_t at = myhist[dg];
+          __syncwarp(act);
+          if (lane == __ffs(same) - 1) myhist[dg] = at + __popc(same);
+          out[base[dg] + at + __popc(same & ((1u << lane) - 1))] = it[j];
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
     // every item is in place, and no CTA still reads another's counts, before the next pass
     cluster_sync();
@@ -181,66 +210,123 @@ __device__ __forceinline__ void add_row8(float* dst, const float (&v)[8], float 
   store8(dst, from_f32<float>(o));
 }
 
-// One thread per (tile of sorted tokens, 8 columns). A row all of whose tokens lie in the
-// tile is finished here. Of a row whose tokens span tiles, the sum of this tile's share goes
-// to part: slot 0 where the row began in an earlier tile, slot 1 where it begins here.
+// A group of `lanes` threads walks `run` sorted tokens, each thread with eight columns of the
+// running sum; a CTA has 256 / lanes neighbouring groups, its tile, and lanes * 8 columns. A
+// row all of whose tokens a group meets is finished by it. Of a row whose tokens span groups,
+// each group's share goes to shared memory, and the group in which the row begins adds the
+// shares up in order; of a row that spans tiles the tile's sum goes to part: slot 0 where the
+// row began in an earlier tile, slot 1 where it begins here.
+constexpr int kHead = 1, kTail = 2, kThrough = 4;  // a share of a row that began before, that goes on, both
+
+constexpr int kAhead = 4;                         // rows of dX loaded at a time
+
 template <typename T>
 __global__ void __launch_bounds__(256)
     embed_grad_kernel(const uint64_t* __restrict__ sorted, int64_t n, int32_t V,
-                      const T* __restrict__ dX, int nvec, int tile_n, float scale, bool accumulate,
-                      float* __restrict__ dW, float* __restrict__ part) {
-  const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t tile = idx / nvec;
-  const int64_t i0 = tile * tile_n;
-  if (i0 >= n) return;
-  const int64_t col = (idx - tile * nvec) * 8, d = (int64_t)nvec * 8;
-  const int64_t i1 = min(n, i0 + tile_n);
-  const int32_t next = i1 < n ? key_of(sorted[i1]) : -1;
-  int32_t cur = key_of(sorted[i0]);
-  bool head = i0 > 0 && key_of(sorted[i0 - 1]) == cur;
+                      const T* __restrict__ dX, int nvec, EmbedShape shape, float scale,
+                      bool accumulate, float* __restrict__ dW, float* __restrict__ part) {
+  __shared__ float4 head_sum[256][2];
+  __shared__ int flags[256];
+  const int lanes = shape.lanes, groups = 256 / lanes;
+  const int g = threadIdx.x / lanes, l = threadIdx.x % lanes;
+  const int64_t tile = blockIdx.x / shape.slabs;  // a tile's slabs run side by side
+  const int vec = (int)(blockIdx.x - tile * shape.slabs) * lanes + l;
+  const int64_t i0 = (tile * groups + g) * shape.run;
+  const int64_t i1 = min(n, i0 + shape.run);
+  const int64_t col = (int64_t)vec * 8, d = (int64_t)nvec * 8;
+  const bool on = vec < nvec;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  auto flush = [&](bool tail) {
-    if (cur == V) return;
-    if (!head && !tail) {
-      add_row8(dW + (int64_t)cur * d + col, acc, scale, accumulate);
-    } else {
-      store8(part + (tile * 2 + (head ? 0 : 1)) * d + col, from_f32<float>(acc));
-    }
+  int32_t cur = V;
+  int flag = 0;
+  auto put_head = [&] {
+    const Raw8<float> r = from_f32<float>(acc);
+    head_sum[threadIdx.x][0] = r.a;
+    head_sum[threadIdx.x][1] = r.b;
   };
-  for (int64_t ib = i0; ib < i1 && cur != V; ib += 4) {
-    int32_t key[4];
-    Raw8<T> r[4];
+  if (i0 < n) {
+    const int32_t next = i1 < n ? key_of(sorted[i1]) : -1;
+    cur = key_of(sorted[i0]);
+    bool head = i0 > 0 && key_of(sorted[i0 - 1]) == cur;
+    for (int64_t ib = i0; ib < i1 && cur != V; ib += kAhead) {
+      int32_t key[kAhead];
+      Raw8<T> r[kAhead];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      key[u] = V;
-      if (ib + u < i1) {
-        const uint64_t it = sorted[ib + u];
-        key[u] = key_of(it);
-        if (key[u] != V) r[u] = load8(dX + (int64_t)(uint32_t)it * d + col);
+      for (int u = 0; u < kAhead; ++u) {
+        key[u] = V;
+        if (ib + u < i1) {
+          const uint64_t it = sorted[ib + u];
+          key[u] = key_of(it);
+          if (on && key[u] != V) r[u] = load8(dX + (int64_t)(uint32_t)it * d + col);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (ib + u >= i1) break;
+        if (key[u] != cur) {
+          if (head) {
+            put_head();
+            flag = kHead;
+          } else if (on) {
+            add_row8(dW + (int64_t)cur * d + col, acc, scale, accumulate);
+          }
+          cur = key[u];
+          head = false;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+        }
+        if (cur == V) break;  // the tokens without a row come last
+        float f[8];
+        to_f32(r[u], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += on ? f[j] : 0.f;
       }
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (ib + u >= i1) break;
-      if (key[u] != cur) {
-        flush(false);
-        cur = key[u];
-        head = false;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    if (cur != V) {
+      const bool tail = cur == next;
+      if (head) {
+        put_head();
+        flag = kHead | (tail ? kThrough : 0);
+      } else if (tail) {
+        flag |= kTail;  // the sum stays in acc
+      } else if (on) {
+        add_row8(dW + (int64_t)cur * d + col, acc, scale, accumulate);
       }
-      if (cur == V) break;  // the tokens without a row come last
-      float f[8];
-      to_f32(r[u], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += f[j];
     }
   }
-  flush(cur == next);
+  if (l == 0) flags[g] = flag;
+  __syncthreads();
+  const bool begins = flag & kTail, goes_on = g == 0 && (flag & kHead);
+  if (!begins && !goes_on) return;  // (a group can be both: two rows)
+  auto follow = [&](int j, bool more) {  // add the shares of the groups from j on; still going on?
+    for (; j < groups && more; ++j) {
+      const Raw8<float> o{head_sum[j * lanes + l][0], head_sum[j * lanes + l][1]};
+      float f[8];
+      to_f32(o, f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] += f[k];
+      more = flags[j] & kThrough;
+    }
+    return more;
+  };
+  float* mine = part + tile * 2 * d + col;
+  if (begins) {
+    if (follow(g + 1, true)) {
+      if (on) store8(mine + d, from_f32<float>(acc));
+    } else if (on) {
+      add_row8(dW + (int64_t)cur * d + col, acc, scale, accumulate);
+    }
+  }
+  if (goes_on) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+    follow(0, true);
+    if (on) store8(mine, from_f32<float>(acc));
+  }
 }
 
-// One CTA per tile; works where a row that spans tiles begins in it: adds up the row's
-// partial sums, each of the eight warps a contiguous share of them, then the eight in order.
+// One CTA per (tile, 256 columns); works where a row that spans tiles begins in the tile: adds
+// up the row's partial sums, each of the eight warps a contiguous share of them, then the
+// eight in order.
 __global__ void __launch_bounds__(256)
     embed_join_kernel(const uint64_t* __restrict__ sorted, int64_t n, int32_t V, int d, int tile_n,
                       float scale, bool accumulate, float* __restrict__ dW,
@@ -251,7 +337,13 @@ __global__ void __launch_bounds__(256)
   const int32_t cur = key_of(sorted[i1 - 1]);
   if (cur == V || key_of(sorted[i1]) != cur) return;
   if (key_of(sorted[i0]) == cur && i0 > 0 && key_of(sorted[i0 - 1]) == cur) return;
-  int64_t lo = i1, hi = n;  // the row's end: first sorted token past i1 with another key
+  // the row's end: tile ends first, doubling the step, then halving it
+  int64_t lo = i1, hi = n, step = tile_n;  // sorted[lo - 1] is the row's, sorted[hi] is not
+  while (lo + step < n && key_of(sorted[lo + step]) == cur) {
+    lo += step;
+    step *= 2;
+  }
+  hi = min(n, lo + step);
   while (lo < hi) {
     const int64_t mid = (lo + hi) >> 1;
     if (key_of(sorted[mid]) == cur) lo = mid + 1; else hi = mid;
@@ -260,33 +352,30 @@ __global__ void __launch_bounds__(256)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t share = (n_part + 7) / 8;
   const int64_t p0 = min(n_part, warp * share), p1 = min(n_part, p0 + share);
-  for (int c0 = 0; c0 < d; c0 += 256) {
-    const int col = c0 + lane * 8;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (col < d) {
-#pragma unroll 4
-      for (int64_t p = p0; p < p1; ++p) {
-        float f[8];
-        to_f32(load8(part + ((tile + p) * 2 + (p == 0 ? 1 : 0)) * d + col), f);
+  const int col = blockIdx.y * 256 + lane * 8;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (col < d) {
+#pragma unroll 8
+    for (int64_t p = p0; p < p1; ++p) {
+      float f[8];
+      to_f32(load8(part + ((tile + p) * 2 + (p == 0 ? 1 : 0)) * d + col), f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += f[j];
-      }
+      for (int j = 0; j < 8; ++j) acc[j] += f[j];
     }
-    const Raw8<float> mine = from_f32<float>(acc);
-    red[warp][lane][0] = mine.a;
-    red[warp][lane][1] = mine.b;
-    __syncthreads();
-    if (warp == 0 && col < d) {
-      for (int w = 1; w < 8; ++w) {
-        const Raw8<float> o{red[w][lane][0], red[w][lane][1]};
-        float f[8];
-        to_f32(o, f);
+  }
+  const Raw8<float> mine = from_f32<float>(acc);
+  red[warp][lane][0] = mine.a;
+  red[warp][lane][1] = mine.b;
+  __syncthreads();
+  if (warp == 0 && col < d) {
+    for (int w = 1; w < 8; ++w) {
+      const Raw8<float> o{red[w][lane][0], red[w][lane][1]};
+      float f[8];
+      to_f32(o, f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += f[j];
-      }
-      add_row8(dW + (int64_t)cur * d + col, acc, scale, accumulate);
+      for (int j = 0; j < 8; ++j) acc[j] += f[j];
     }
-    __syncthreads();
+    add_row8(dW + (int64_t)cur * d + col, acc, scale, accumulate);
   }
 }
 
@@ -321,7 +410,8 @@ int embed_sort_result(int32_t V) {
   return n_pass % 2 == 0 ? 1 : 0;
 }
 
-cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_b, cudaStream_t s) {
+cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_b, float* fill,
+                              int64_t n_fill, int num_sms, cudaStream_t s) {
   int n_pass, bits;
   sort_digits(a.V, n_pass, bits);
   int cluster = 1;  // about a thousand items per CTA, at most the portable cluster size
@@ -335,41 +425,57 @@ cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_
   attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)cluster, 1, 1);
+  // the rest of the SMs to the zeros, in whole clusters (64 KB of dW at least for a block)
+  const int64_t zero = std::min<int64_t>(std::max(0, num_sms / cluster - 1), n_fill / 16384 / cluster + 1);
+  cfg.gridDim = dim3((unsigned)(cluster * (1 + (n_fill ? std::max<int64_t>(1, zero) : 0))), 1, 1);
   cfg.blockDim = dim3(kSortWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = kSortSmem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a, n_pass, bits, cluster, buf_a, buf_b);
+  return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a, n_pass, bits, cluster, buf_a, buf_b,
+                            reinterpret_cast<float4*>(fill), n_fill / 4);
 }
 
-// Longer tiles mean fewer partial rows, shorter ones more threads: the longest that still
-// fills the GPU's threads once.
-int embed_tile(int64_t T, int d, int num_sms) {
-  int tile = 32;
-  while (tile > 4 && (T + tile - 1) / tile * (d / 8) < (int64_t)num_sms * 2048) tile /= 2;
-  return tile;
+// Lanes of a group: as many as a row has vectors of eight columns, or the most of 32, 16 and 8 that
+// leave at most a quarter idle (at d = 2880: 32 lanes 12 of 384 idle, 90 us; 8 lanes none, 164 us, as
+// they read 128 bytes of a row at a time). Tokens of a group: the most, up to 16, that still give every SM two
+// rounds of eight CTAs (a longer walk leaves fewer partial sums, a shorter one more in parallel).
+EmbedShape embed_shape(int64_t T, int d, int num_sms) {
+  const int nvec = d / 8;
+  EmbedShape p;
+  p.lanes = 1;
+  if (nvec < 8) {
+    while (p.lanes < nvec) p.lanes *= 2;
+  } else {
+    p.lanes = 32;
+    while (p.lanes > 8 && (nvec + p.lanes - 1) / p.lanes * p.lanes * 3 > nvec * 4) p.lanes /= 2;
+  }
+  p.slabs = (nvec + p.lanes - 1) / p.lanes;
+  p.run = 16;
+  auto tiles = [&] { return (T + (int64_t)p.tile() - 1) / p.tile(); };
+  while (p.run > 4 && tiles() * p.slabs < (int64_t)num_sms * 16) p.run /= 2;
+  return p;
 }
 
 void launch_embed_grad(const uint64_t* sorted, int64_t T, int32_t V, bool bf16, const void* dX,
-                       int d, int tile, float scale, bool accumulate, float* dW, float* part,
-                       cudaStream_t s) {
-  const int64_t threads = (T + tile - 1) / tile * (d / 8);
-  const unsigned blocks = (unsigned)((threads + 255) / 256);
+                       int d, const EmbedShape& p, float scale, bool accumulate, float* dW,
+                       float* part, cudaStream_t s) {
+  const unsigned grid = (unsigned)((T + p.tile() - 1) / p.tile() * p.slabs);
   if (bf16)
-    embed_grad_kernel<uint16_t><<<blocks, 256, 0, s>>>(sorted, T, V, (const uint16_t*)dX, d / 8,
-                                                       tile, scale, accumulate, dW, part);
+    embed_grad_kernel<uint16_t><<<grid, 256, 0, s>>>(sorted, T, V, (const uint16_t*)dX, d / 8, p,
+                                                     scale, accumulate, dW, part);
   else
-    embed_grad_kernel<float><<<blocks, 256, 0, s>>>(sorted, T, V, (const float*)dX, d / 8, tile,
-                                                    scale, accumulate, dW, part);
+    embed_grad_kernel<float><<<grid, 256, 0, s>>>(sorted, T, V, (const float*)dX, d / 8, p, scale,
+                                                  accumulate, dW, part);
 }
 
-void launch_embed_join(const uint64_t* sorted, int64_t T, int32_t V, int d, int tile, float scale,
-                       bool accumulate, float* dW, const float* part, cudaStream_t s) {
-  const int64_t tiles = (T + tile - 1) / tile;
-  embed_join_kernel<<<(unsigned)tiles, 256, 0, s>>>(sorted, T, V, d, tile, scale, accumulate, dW,
-                                                    part);
+void launch_embed_join(const uint64_t* sorted, int64_t T, int32_t V, int d, const EmbedShape& p,
+                       float scale, bool accumulate, float* dW, const float* part, cudaStream_t s) {
+  const int64_t tiles = (T + p.tile() - 1) / p.tile();
+  if (tiles < 2) return;  // no row spans tiles
+  embed_join_kernel<<<dim3((unsigned)tiles, (unsigned)((d + 255) / 256)), 256, 0, s>>>(
+      sorted, T, V, d, p.tile(), scale, accumulate, dW, part);
 }
 
 }  // namespace ckl

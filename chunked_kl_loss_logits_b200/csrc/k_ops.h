@@ -22,17 +22,25 @@ struct EmbedIds {
 void launch_embed(const EmbedIds& a, bool bf16, const void* W, int d, float scale, void* out,
                   bool out_f32, cudaStream_t s);
 // (row, position) of every token in ascending order, as row << 32 | position; the row is V for
-// tokens that have none here. The result is in `b` if the return value is 1, else in `a`.
+// tokens that have none here. The result is in `b` where embed_sort_result is 1, else in `a`.
+// The same launch zeroes n_fill floats (a multiple of 8) at `fill`.
 int embed_sort_result(int32_t V);
-cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_b, cudaStream_t s);
-int embed_tile(int64_t T, int d, int num_sms);  // sorted tokens a thread walks
+cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_b, float* fill,
+                              int64_t n_fill, int num_sms, cudaStream_t s);
+// How the gradient is shared out: groups of `lanes` threads walk `run` sorted tokens each,
+// 256 / lanes groups make a CTA's tile, `slabs` CTAs cover the columns.
+struct EmbedShape {
+  int lanes, run, slabs;
+  __host__ __device__ int tile() const { return 256 / lanes * run; }
+};
+EmbedShape embed_shape(int64_t T, int d, int num_sms);
 // dW[row] (+)= scale * sum of the row's dX, in order of position. part: 2 fp32 rows for each
 // tile, the sums of rows whose tokens span tiles; launch_embed_join adds those up.
 void launch_embed_grad(const uint64_t* sorted, int64_t T, int32_t V, bool bf16, const void* dX,
-                       int d, int tile, float scale, bool accumulate, float* dW, float* part,
-                       cudaStream_t s);
-void launch_embed_join(const uint64_t* sorted, int64_t T, int32_t V, int d, int tile, float scale,
-                       bool accumulate, float* dW, const float* part, cudaStream_t s);
+                       int d, const EmbedShape& p, float scale, bool accumulate, float* dW,
+                       float* part, cudaStream_t s);
+void launch_embed_join(const uint64_t* sorted, int64_t T, int32_t V, int d, const EmbedShape& p,
+                       float scale, bool accumulate, float* dW, const float* part, cudaStream_t s);
 
 // ---- 8-bit checkpoints and the norm (k_act8.cu)
 void launch_act8_pack(bool bf16, const void* X, int64_t T, int cols, int fmt, uint8_t* q,
@@ -53,9 +61,9 @@ struct NormArgs {
   float* rstd;
   float* part;           // backward: dgain partials, norm_part_rows x d
 };
-void launch_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t s);
-int64_t norm_part_rows(int64_t T, int d, int num_sms);
-void launch_norm_bwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s);
+int64_t norm_part_rows(int64_t T, int d, bool bf16, int num_sms);
+cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s);
 // out[c] (+)= sum over rows of part[r][c], in a fixed order
 void launch_norm_dgain(const float* part, int64_t rows, int d, bool accumulate, float* out,
                        cudaStream_t s);

@@ -90,6 +90,38 @@ __device__ __forceinline__ Raw8<T> zero8() {
   return from_f32<T>(z);
 }
 
+// Copies of 16 or 8 bytes to shared memory that go on while the thread does; a thread waits for
+// its own, in groups.
+template <int N>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+  static_assert(N == 16 || N == 8, "");
+  if (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Wait until at most N of this thread's groups are under way.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+// Eight elements by cp.async, and back from there.
+__device__ __forceinline__ void copy8(Raw8<uint16_t>* dst, const uint16_t* src) {
+  cp_async<16>(dst, src);
+}
+__device__ __forceinline__ void copy8(Raw8<float>* dst, const float* src) {
+  cp_async<16>(&dst->a, src);
+  cp_async<16>(&dst->b, src + 4);
+}
+
 __device__ __forceinline__ float warp_add(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -134,10 +166,12 @@ __device__ __forceinline__ uint2 act8_encode(const float (&v)[8], uint32_t byte,
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (fmt == kActInt8) {
+      // 1.5 * 2^23 + u rounds u to a whole number, whose two's complement is in the low bits
+      // (conversion instructions run at a quarter of the rate)
       uint32_t c[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = (uint32_t)__float2int_rn(u[4 * j + i]) & 0xFFu;
-      w[j] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+      for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(__fadd_rn(u[4 * j + i], 12582912.f));
+      w[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     } else {
       const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(u[4 * j], u[4 * j + 1]),
                                                    __NV_SATFINITE, __NV_E4M3);
@@ -156,8 +190,11 @@ __device__ __forceinline__ void act8_decode(uint2 q, float scale, int fmt, float
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (fmt == kActInt8) {
+      // a code's byte with its sign bit flipped, in the low bits of 2^23, is 2^23 + 128 + code
+      const uint32_t x = w[j] ^ 0x80808080u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * j + i] = (float)(int8_t)(w[j] >> (8 * i)) * scale;
+      for (int i = 0; i < 4; ++i)
+        v[4 * j + i] = (__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7550 + i)) - 8388736.f) * scale;
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {

@@ -21,7 +21,7 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 # one vector of 8 columns; ragged last blocks; every count of warps and vectors a row takes
-WIDTHS = [8, 24, 40, 136, 264, 520, 1032, 2048, 2880, 4104, 8192, 12000]
+WIDTHS = [8, 24, 40, 136, 264, 520, 1032, 2048, 2880, 4104, 8192, 12000, 24000]
 
 
 def rows(T, d, dt, seed=0):
@@ -96,6 +96,8 @@ def test_unpack_reads_every_code_and_scale(fmt):
 @pytest.mark.parametrize("d", WIDTHS)
 @pytest.mark.parametrize("residual", [False, True])
 def test_norm_forward_and_backward(d, dt, residual):
+    if dt == "f32" and d > 12800:
+        pytest.skip("no fp32 handle has rows this wide")
     for T, fmt in ((1, "int8"), (3, "e4m3"), (37, "int8")):
         x, r = rows(T, d, dt), rows(T, d, dt, 1) if residual else None
         gain = (1 + 0.2 * torch.randn(d, device="cuda")).to(DT[dt])
