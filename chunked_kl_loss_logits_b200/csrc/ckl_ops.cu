@@ -266,15 +266,16 @@ ckl_status ckl_embed_grad(ckl_handle h, const int32_t* ids, const uint8_t* mask,
     Launcher L{h, s};
     const int64_t n_fill = accumulate ? 0 : (int64_t)V * d;
     chk(L(KID_EMBED_SORT, 0, (double)T * 12 + 4.0 * n_fill, [&] {
-      chk(launch_embed_sort(ids_of(h, ids, mask, T, V_total, v0), a, b, dW, n_fill, h->num_sms, s));
+      chk(launch_embed_sort(ids_of(h, ids, mask, T, V_total, v0), a, b, dW, n_fill, s));
     }));
     chk(L(KID_EMBED_GRAD, 0, (double)T * d * elem(h), [&] {
-      launch_embed_grad(sorted, T, V, h->dtype == CKL_BF16, dX, d, P.shape, scale, accumulate != 0,
-                        dW, part, s);
+      chk(launch_embed_grad(sorted, T, V, h->dtype == CKL_BF16, dX, d, P.shape, scale,
+                            accumulate != 0, dW, part, s));
     }));
-    chk(L(KID_EMBED_JOIN, 0, 0, [&] {
-      launch_embed_join(sorted, T, V, d, P.shape, scale, accumulate != 0, dW, part, s);
-    }));
+    if (T > P.shape.tile())  // a row may span tiles
+      chk(L(KID_EMBED_JOIN, 0, 0, [&] {
+        chk(launch_embed_join(sorted, T, V, d, P.shape, scale, accumulate != 0, dW, part, s));
+      }));
   }
   if ((st = cuda_status(err)) != CKL_OK) return st;
   return wait ? sync_and_read(h, s, nullptr, nullptr) : CKL_OK;

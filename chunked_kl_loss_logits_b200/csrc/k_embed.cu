@@ -20,16 +20,12 @@ namespace ckl {
 
 namespace {
 
-// The token's row among those held here, or V (mask 0, another rank's row, or out of range).
-__device__ __forceinline__ int32_t token_row(const EmbedIds& a, int64_t t, bool& bad) {
-  if (a.mask && a.mask[t] == 0) return a.V;
-  const int32_t id = a.ids[t];
-  if (id < 0 || id >= a.V_total) {
-    bad = true;
-    return a.V;
-  }
+// A token's row among those held here, or V (mask 0, another rank's row, or out of range).
+__device__ __forceinline__ int32_t row_of(const EmbedIds& a, int32_t id, uint8_t keep, bool& bad) {
   const int32_t r = id - a.v0;
-  return r >= 0 && r < a.V ? r : a.V;
+  const bool in = id >= 0 && id < a.V_total;
+  bad |= keep && !in;
+  return keep && in && r >= 0 && r < a.V ? r : a.V;
 }
 
 // One warp per (token, 128 vectors of 8 columns).
@@ -43,7 +39,7 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedIds a, const T* _
   if (t >= a.T) return;
   const int v0 = (int)(w - t * slabs) * 128 + lane;
   bool bad = false;
-  const int32_t row = token_row(a, t, bad);
+  const int32_t row = row_of(a, a.ids[t], a.mask ? a.mask[t] : 1, bad);
   if (bad && lane == 0) atomicOr(a.status, (unsigned)ST_INDEX_RANGE);
   const bool have = row < a.V;
   const T* src = W + (int64_t)(have ? row : 0) * nvec * 8;
@@ -72,9 +68,10 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedIds a, const T* _
 // digits, then over warps" gives every item its place, and equal keys keep their order.
 // The digit counts of the other CTAs are read from their shared memory.
 constexpr int kSortWarps = 32;
-constexpr int kBatch = 8;
+constexpr int kBatch = 4;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxBins = 1 << kMaxDigitBits;
+constexpr int kFillBlock = 16384;  // 16-byte vectors of dW that a block zeroes
 constexpr size_t kSortSmem = (size_t)(kSortWarps * kMaxBins + 2 * kMaxBins + 32) * 4;
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -83,15 +80,25 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
+// The two halves of a cluster barrier that orders no memory.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // The first cluster sorts. The others (where dW is to be overwritten) zero dW meanwhile.
 __global__ void __launch_bounds__(kSortWarps * 32, 1)
     embed_sort_kernel(const EmbedIds a, int n_pass, int bits, int cluster, uint64_t* buf_a,
                       uint64_t* buf_b, float4* fill, int64_t n_fill) {
   extern __shared__ uint32_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_launch_dependents();
   if (blockIdx.x >= cluster) {
-    const int64_t step = (int64_t)(gridDim.x - cluster) * blockDim.x;
-    for (int64_t i = (int64_t)(blockIdx.x - cluster) * blockDim.x + tid; i < n_fill; i += step)
+    const int64_t i0 = (int64_t)(blockIdx.x - cluster) * kFillBlock + tid;
+#pragma unroll 8
+    for (int64_t i = i0; i < min(n_fill, i0 - tid + kFillBlock); i += kSortWarps * 32)
       fill[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     return;
   }
@@ -115,18 +122,31 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
     // kBatch items a lane at a time; a warp's range of at most one batch stays in registers
     uint64_t it[kBatch];
     auto load = [&](int64_t ib) {
+      if (p == 0) {
+        int32_t id[kBatch];
+        uint8_t keep[kBatch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int64_t i = ib + j * 32 + lane;
-        if (i >= i1) continue;
-        it[j] = p == 0 ? (uint64_t)(uint32_t)token_row(a, i, bad) << 32 | (uint64_t)i
-                       : __ldcg(reinterpret_cast<const unsigned long long*>(in) + i);
+        for (int j = 0; j < kBatch; ++j) {
+          const int64_t i = min(ib + j * 32 + lane, i1 - 1);
+          id[j] = a.ids[i];
+          keep[j] = a.mask ? a.mask[i] : 1;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          it[j] = (uint64_t)(uint32_t)row_of(a, id[j], keep[j], bad) << 32 |
+                  (uint64_t)(ib + j * 32 + lane);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          it[j] = __ldcg(reinterpret_cast<const unsigned long long*>(in) +
+                         min(ib + j * 32 + lane, i1 - 1));
       }
     };
     auto digit = [&](uint64_t v) { return (uint32_t)(v >> shift) & (uint32_t)(bins - 1); };
     if (i0 < i1) load(i0);
     for (int b = lane; b < bins; b += 32) myhist[b] = 0;
     __syncwarp();
+#pragma unroll 1
     for (int64_t ib = i0; ib < i1; ib += kBatch * 32) {
       if (ib > i0) load(ib);
 #pragma unroll
@@ -154,6 +174,9 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
         all += c;
       }
     }
+    // the other CTAs' counts are read: after the last pass nothing else keeps a CTA from leaving
+    const bool last = p == n_pass - 1;
+    if (last) cluster_arrive();
     // exclusive prefix of `all` over the bins (threads past the bins hold 0)
     uint32_t incl = all;
 #pragma unroll
@@ -169,6 +192,7 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
       base[tid] = pre + incl - all + before;
     }
     __syncthreads();
+#pragma unroll 1
     for (int64_t ib = i0; ib < i1; ib += kBatch * 32) {
       if (i1 - i0 > kBatch * 32) load(ib);
 #pragma unroll
@@ -188,7 +212,8 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
       }
     }
     // every item is in place, and no CTA still reads another's counts, before the next pass
-    cluster_sync();
+    if (last) cluster_wait();
+    else cluster_sync();
   }
   if (bad) atomicOr(a.status, (unsigned)ST_INDEX_RANGE);
 }
@@ -196,18 +221,22 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
 // ------------------------------------------------------------------ gradient
 __device__ __forceinline__ int32_t key_of(uint64_t it) { return (int32_t)(it >> 32); }
 
+// dst (+)= scale * v. The addition is made in L2, so that the thread does not wait for the old
+// value; a call adds to an element once, so it is the sum of two numbers either way.
 __device__ __forceinline__ void add_row8(float* dst, const float (&v)[8], float scale,
                                          bool accumulate) {
   float o[8];
-  if (accumulate) {
-    to_f32(load8(dst), o);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] += scale * v[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = scale * v[j];
+  for (int j = 0; j < 8; ++j) o[j] = scale * v[j];
+  if (!accumulate) {
+    store8(dst, from_f32<float>(o));
+    return;
   }
-  store8(dst, from_f32<float>(o));
+#pragma unroll
+  for (int j = 0; j < 8; j += 4)
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + j), "f"(o[j]),
+                 "f"(o[j + 1]), "f"(o[j + 2]), "f"(o[j + 3])
+                 : "memory");
 }
 
 // A group of `lanes` threads walks `run` sorted tokens, each thread with eight columns of the
@@ -231,6 +260,8 @@ __global__ void __launch_bounds__(256)
   const int g = threadIdx.x / lanes, l = threadIdx.x % lanes;
   const int64_t tile = blockIdx.x / shape.slabs;  // a tile's slabs run side by side
   const int vec = (int)(blockIdx.x - tile * shape.slabs) * lanes + l;
+  griddep_wait();
+  griddep_launch_dependents();
   const int64_t i0 = (tile * groups + g) * shape.run;
   const int64_t i1 = min(n, i0 + shape.run);
   const int64_t col = (int64_t)vec * 8, d = (int64_t)nvec * 8;
@@ -333,22 +364,23 @@ __global__ void __launch_bounds__(256)
                       const float* __restrict__ part) {
   __shared__ float4 red[8][32][2];
   const int64_t tile = blockIdx.x, i0 = tile * tile_n, i1 = i0 + tile_n;
+  griddep_wait();
   if (i1 >= n) return;
   const int32_t cur = key_of(sorted[i1 - 1]);
   if (cur == V || key_of(sorted[i1]) != cur) return;
   if (key_of(sorted[i0]) == cur && i0 > 0 && key_of(sorted[i0 - 1]) == cur) return;
-  // the row's end: tile ends first, doubling the step, then halving it
-  int64_t lo = i1, hi = n, step = tile_n;  // sorted[lo - 1] is the row's, sorted[hi] is not
-  while (lo + step < n && key_of(sorted[lo + step]) == cur) {
+  // the tiles after this one that begin with the row: doubling the step, then halving it
+  auto goes_on = [&](int64_t k) {
+    return (tile + k) * tile_n < n && key_of(sorted[(tile + k) * tile_n]) == cur;
+  };
+  int64_t lo = 1, step = 1;  // tile + lo begins with the row
+  while (goes_on(lo + step)) {
     lo += step;
     step *= 2;
   }
-  hi = min(n, lo + step);
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (key_of(sorted[mid]) == cur) lo = mid + 1; else hi = mid;
-  }
-  const int64_t n_part = (lo - 1) / tile_n - tile + 1;  // slot 1 of this tile, slot 0 of the others
+  for (; step > 1; step /= 2)
+    if (goes_on(lo + step / 2)) lo += step / 2;
+  const int64_t n_part = lo + 1;  // slot 1 of this tile, slot 0 of the others
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t share = (n_part + 7) / 8;
   const int64_t p0 = min(n_part, warp * share), p1 = min(n_part, p0 + share);
@@ -411,7 +443,7 @@ int embed_sort_result(int32_t V) {
 }
 
 cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_b, float* fill,
-                              int64_t n_fill, int num_sms, cudaStream_t s) {
+                              int64_t n_fill, cudaStream_t s) {
   int n_pass, bits;
   sort_digits(a.V, n_pass, bits);
   int cluster = 1;  // about a thousand items per CTA, at most the portable cluster size
@@ -425,9 +457,11 @@ cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_
   attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  // the rest of the SMs to the zeros, in whole clusters (64 KB of dW at least for a block)
-  const int64_t zero = std::min<int64_t>(std::max(0, num_sms / cluster - 1), n_fill / 16384 / cluster + 1);
-  cfg.gridDim = dim3((unsigned)(cluster * (1 + (n_fill ? std::max<int64_t>(1, zero) : 0))), 1, 1);
+  // Blocks of zeros in whole clusters, many more than fit at once: where the GPU's parts do not
+  // divide into clusters some SMs hold fewer, so a fixed share for each would end late (a grid of
+  // one block per SM: 58 us for 262 MB, this 41).
+  const int64_t zero = (n_fill / 4 + kFillBlock - 1) / kFillBlock;
+  cfg.gridDim = dim3((unsigned)(cluster * (1 + (zero + cluster - 1) / cluster)), 1, 1);
   cfg.blockDim = dim3(kSortWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = kSortSmem;
   cfg.stream = s;
@@ -458,24 +492,22 @@ EmbedShape embed_shape(int64_t T, int d, int num_sms) {
   return p;
 }
 
-void launch_embed_grad(const uint64_t* sorted, int64_t T, int32_t V, bool bf16, const void* dX,
-                       int d, const EmbedShape& p, float scale, bool accumulate, float* dW,
-                       float* part, cudaStream_t s) {
-  const unsigned grid = (unsigned)((T + p.tile() - 1) / p.tile() * p.slabs);
-  if (bf16)
-    embed_grad_kernel<uint16_t><<<grid, 256, 0, s>>>(sorted, T, V, (const uint16_t*)dX, d / 8, p,
-                                                     scale, accumulate, dW, part);
-  else
-    embed_grad_kernel<float><<<grid, 256, 0, s>>>(sorted, T, V, (const float*)dX, d / 8, p, scale,
-                                                  accumulate, dW, part);
+cudaError_t launch_embed_grad(const uint64_t* sorted, int64_t T, int32_t V, bool bf16,
+                              const void* dX, int d, const EmbedShape& p, float scale,
+                              bool accumulate, float* dW, float* part, cudaStream_t s) {
+  const dim3 grid((unsigned)((T + p.tile() - 1) / p.tile() * p.slabs));
+  return bf16 ? launch_behind(embed_grad_kernel<uint16_t>, grid, 256, 0, s, sorted, T, V,
+                              (const uint16_t*)dX, d / 8, p, scale, accumulate, dW, part)
+              : launch_behind(embed_grad_kernel<float>, grid, 256, 0, s, sorted, T, V,
+                              (const float*)dX, d / 8, p, scale, accumulate, dW, part);
 }
 
-void launch_embed_join(const uint64_t* sorted, int64_t T, int32_t V, int d, const EmbedShape& p,
-                       float scale, bool accumulate, float* dW, const float* part, cudaStream_t s) {
-  const int64_t tiles = (T + p.tile() - 1) / p.tile();
-  if (tiles < 2) return;  // no row spans tiles
-  embed_join_kernel<<<dim3((unsigned)tiles, (unsigned)((d + 255) / 256)), 256, 0, s>>>(
-      sorted, T, V, d, p.tile(), scale, accumulate, dW, part);
+cudaError_t launch_embed_join(const uint64_t* sorted, int64_t T, int32_t V, int d,
+                              const EmbedShape& p, float scale, bool accumulate, float* dW,
+                              const float* part, cudaStream_t s) {
+  const dim3 grid((unsigned)((T + p.tile() - 1) / p.tile()), (unsigned)((d + 255) / 256));
+  return launch_behind(embed_join_kernel, grid, 256, 0, s, sorted, T, V, d, p.tile(), scale,
+                       accumulate, dW, part);
 }
 
 }  // namespace ckl

@@ -26,7 +26,7 @@ void launch_embed(const EmbedIds& a, bool bf16, const void* W, int d, float scal
 // The same launch zeroes n_fill floats (a multiple of 8) at `fill`.
 int embed_sort_result(int32_t V);
 cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_b, float* fill,
-                              int64_t n_fill, int num_sms, cudaStream_t s);
+                              int64_t n_fill, cudaStream_t s);
 // How the gradient is shared out: groups of `lanes` threads walk `run` sorted tokens each,
 // 256 / lanes groups make a CTA's tile, `slabs` CTAs cover the columns.
 struct EmbedShape {
@@ -36,11 +36,13 @@ struct EmbedShape {
 EmbedShape embed_shape(int64_t T, int d, int num_sms);
 // dW[row] (+)= scale * sum of the row's dX, in order of position. part: 2 fp32 rows for each
 // tile, the sums of rows whose tokens span tiles; launch_embed_join adds those up.
-void launch_embed_grad(const uint64_t* sorted, int64_t T, int32_t V, bool bf16, const void* dX,
-                       int d, const EmbedShape& p, float scale, bool accumulate, float* dW,
-                       float* part, cudaStream_t s);
-void launch_embed_join(const uint64_t* sorted, int64_t T, int32_t V, int d, const EmbedShape& p,
-                       float scale, bool accumulate, float* dW, const float* part, cudaStream_t s);
+// Both are launched behind the kernel before them (launch_behind).
+cudaError_t launch_embed_grad(const uint64_t* sorted, int64_t T, int32_t V, bool bf16,
+                              const void* dX, int d, const EmbedShape& p, float scale,
+                              bool accumulate, float* dW, float* part, cudaStream_t s);
+cudaError_t launch_embed_join(const uint64_t* sorted, int64_t T, int32_t V, int d,
+                              const EmbedShape& p, float scale, bool accumulate, float* dW,
+                              const float* part, cudaStream_t s);
 
 // ---- 8-bit checkpoints and the norm (k_act8.cu)
 void launch_act8_pack(bool bf16, const void* X, int64_t T, int cols, int fmt, uint8_t* q,

@@ -36,6 +36,24 @@ cudaError_t smem_once(F* fn, size_t bytes, std::atomic<uint64_t>& set) {
   return e;
 }
 
+// Launch behind the kernel just enqueued on s, which it may overlap up to its griddep_wait(): the
+// kernel calls that before it touches what the one before wrote or reads what that may write.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*fn)(P...), dim3 grid, unsigned threads, size_t smem,
+                          cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+
 constexpr int kActInt8 = 0, kActE4m3 = 1;  // ckl_act8_format
 constexpr int kActBlock = 32;
 
