@@ -20,11 +20,12 @@ namespace ckl {
 
 namespace {
 
+constexpr int kNoCkpt = -1;
 constexpr int kSlab = 128;  // vectors of eight columns a warp handles of one row (pack, unpack)
 
-template <typename T>
+template <typename T, int FMT>
 __global__ void __launch_bounds__(256)
-    act8_pack_kernel(const T* __restrict__ X, int64_t rows, int nvec, int slabs, int fmt,
+    act8_pack_kernel(const T* __restrict__ X, int64_t rows, int nvec, int slabs,
                      uint8_t* __restrict__ q, uint8_t* __restrict__ e) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -43,18 +44,18 @@ __global__ void __launch_bounds__(256)
     const int v = v0 + i * 32;
     float f[8];
     to_f32(r[i], f);
-    const uint32_t byte = act8_scale_byte(quad_max(amax_bits8(f)), fmt);
+    const uint32_t byte = act8_scale_byte<FMT>(quad_max(amax_bits8(r[i])));
     if (v < nvec) {
-      *reinterpret_cast<uint2*>(q + (t * nvec + v) * 8) = act8_encode(f, byte, fmt);
+      *reinterpret_cast<uint2*>(q + (t * nvec + v) * 8) = act8_encode<FMT>(f, byte);
       if ((lane & 3) == 0) e[t * nb + (v >> 2)] = (uint8_t)byte;
     }
   }
 }
 
-template <typename T>
+template <typename T, int FMT>
 __global__ void __launch_bounds__(256)
     act8_unpack_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ e, int64_t rows,
-                       int nvec, int slabs, int fmt, T* __restrict__ out) {
+                       int nvec, int slabs, T* __restrict__ out) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int64_t t = w / slabs;
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(256)
     const int v = v0 + i * 32;
     if (v >= nvec) break;
     float f[8];
-    act8_decode(c[i], act8_scale(b[i]), fmt, f);
+    act8_decode<FMT>(c[i], act8_scale(b[i]), f);
     store8(out + (t * nvec + v) * 8, from_f32<T>(f));
   }
 }
@@ -110,7 +111,7 @@ __device__ __forceinline__ float row_add(float v, float* red, int warp, int lane
   return t;
 }
 
-template <typename T, int WPR, int VPT>
+template <typename T, int WPR, int VPT, int FMT>  // FMT: the checkpoint's format or kNoCkpt
 __global__ void __launch_bounds__(WPR * 32, NormCfg<T, WPR, VPT, false>::kPerSm)
     norm_fwd_kernel(const NormArgs a) {
   using C = NormCfg<T, WPR, VPT, false>;
@@ -174,10 +175,10 @@ __global__ void __launch_bounds__(WPR * 32, NormCfg<T, WPR, VPT, false>::kPerSm)
       const bool ok = vec(i) < nvec;
       float f[8];
       to_f32(s[i], f);
-      if (a.q) {
-        const uint32_t byte = act8_scale_byte(quad_max(amax_bits8(f)), a.fmt);
+      if (FMT != kNoCkpt) {
+        const uint32_t byte = act8_scale_byte<FMT>(quad_max(amax_bits8(s[i])));
         if (ok) {
-          *reinterpret_cast<uint2*>(a.q + t * a.d + vec(i) * 8) = act8_encode(f, byte, a.fmt);
+          *reinterpret_cast<uint2*>(a.q + t * a.d + vec(i) * 8) = act8_encode<FMT>(f, byte);
           if ((lane & 3) == 0) a.e[t * nb + (vec(i) >> 2)] = (uint8_t)byte;
         }
       }
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(WPR * 32, NormCfg<T, WPR, VPT, false>::kPerSm)
 
 // Keeps its columns' share of dg in registers and leaves it as one line of partial sums, added
 // up by norm_dgain_kernel.
-template <typename T, int WPR, int VPT>
+template <typename T, int WPR, int VPT, int FMT>
 __global__ void __launch_bounds__(WPR * 32, NormCfg<T, WPR, VPT, true>::kPerSm)
     norm_bwd_kernel(const NormArgs a) {
   using C = NormCfg<T, WPR, VPT, true>;
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(WPR * 32, NormCfg<T, WPR, VPT, true>::kPerSm)
     for (int i = 0; i < VPT; ++i) {
       const bool ok = vec(i) < nvec;
       dy[i] = ok ? *slot(stage, 0, i) : zero8<T>();
-      act8_decode(ok ? *qslot(stage, i) : make_uint2(0u, 0u), act8_scale(e[i]), a.fmt, h[i]);
+      act8_decode<FMT>(ok ? *qslot(stage, i) : make_uint2(0u, 0u), act8_scale(e[i]), h[i]);
       float d[8], w[8];
       to_f32(dy[i], d);
       to_f32(g[i], w);
@@ -350,7 +351,7 @@ int64_t norm_blocks(int64_t T_, int d, int num_sms) {
   return T_ < most ? T_ : most;
 }
 
-template <typename T>
+template <typename T, int FMT>
 cudaError_t norm_fwd(const NormArgs& a, int num_sms, cudaStream_t s) {
   const unsigned blocks = (unsigned)norm_blocks<T, false>(a.T, a.d, num_sms);
   cudaError_t err = cudaErrorInvalidValue;
@@ -358,14 +359,14 @@ cudaError_t norm_fwd(const NormArgs& a, int num_sms, cudaStream_t s) {
     constexpr int WPR = decltype(w)::value, VPT = decltype(v)::value;
     using C = NormCfg<T, WPR, VPT, false>;
     static std::atomic<uint64_t> attr_set{0};
-    err = smem_once(norm_fwd_kernel<T, WPR, VPT>, C::kSmem, attr_set);
+    err = smem_once(norm_fwd_kernel<T, WPR, VPT, FMT>, C::kSmem, attr_set);
     if (err == cudaSuccess)
-      norm_fwd_kernel<T, WPR, VPT><<<blocks, C::kThreads, C::kSmem, s>>>(a);
+      norm_fwd_kernel<T, WPR, VPT, FMT><<<blocks, C::kThreads, C::kSmem, s>>>(a);
   });
   return err;
 }
 
-template <typename T>
+template <typename T, int FMT>
 cudaError_t norm_bwd(const NormArgs& a, int num_sms, cudaStream_t s) {
   const unsigned blocks = (unsigned)norm_blocks<T, true>(a.T, a.d, num_sms);
   cudaError_t err = cudaErrorInvalidValue;
@@ -373,37 +374,54 @@ cudaError_t norm_bwd(const NormArgs& a, int num_sms, cudaStream_t s) {
     constexpr int WPR = decltype(w)::value, VPT = decltype(v)::value;
     using C = NormCfg<T, WPR, VPT, true>;
     static std::atomic<uint64_t> attr_set{0};
-    err = smem_once(norm_bwd_kernel<T, WPR, VPT>, C::kSmem, attr_set);
+    err = smem_once(norm_bwd_kernel<T, WPR, VPT, FMT>, C::kSmem, attr_set);
     if (err == cudaSuccess)
-      norm_bwd_kernel<T, WPR, VPT><<<blocks, C::kThreads, C::kSmem, s>>>(a);
+      norm_bwd_kernel<T, WPR, VPT, FMT><<<blocks, C::kThreads, C::kSmem, s>>>(a);
   });
   return err;
+}
+
+template <typename T, int FMT>
+void pack(const void* X, int64_t rows, int nvec, uint8_t* q, uint8_t* e, cudaStream_t s) {
+  const int slabs = (nvec + kSlab - 1) / kSlab;
+  act8_pack_kernel<T, FMT><<<(unsigned)((rows * slabs + 7) / 8), 256, 0, s>>>(
+      static_cast<const T*>(X), rows, nvec, slabs, q, e);
+}
+
+template <typename T, int FMT>
+void unpack(const uint8_t* q, const uint8_t* e, int64_t rows, int nvec, void* out, cudaStream_t s) {
+  const int slabs = (nvec + kSlab - 1) / kSlab;
+  act8_unpack_kernel<T, FMT><<<(unsigned)((rows * slabs + 7) / 8), 256, 0, s>>>(
+      q, e, rows, nvec, slabs, static_cast<T*>(out));
 }
 
 }  // namespace
 
 void launch_act8_pack(bool bf16, const void* X, int64_t T, int cols, int fmt, uint8_t* q,
                       uint8_t* e, cudaStream_t s) {
-  const int nvec = cols / 8, slabs = (nvec + kSlab - 1) / kSlab;
-  const unsigned blocks = (unsigned)((T * slabs + 7) / 8);
-  if (bf16)
-    act8_pack_kernel<uint16_t><<<blocks, 256, 0, s>>>((const uint16_t*)X, T, nvec, slabs, fmt, q, e);
+  if (fmt == kActInt8)
+    bf16 ? pack<uint16_t, kActInt8>(X, T, cols / 8, q, e, s) : pack<float, kActInt8>(X, T, cols / 8, q, e, s);
   else
-    act8_pack_kernel<float><<<blocks, 256, 0, s>>>((const float*)X, T, nvec, slabs, fmt, q, e);
+    bf16 ? pack<uint16_t, kActE4m3>(X, T, cols / 8, q, e, s) : pack<float, kActE4m3>(X, T, cols / 8, q, e, s);
 }
 
 void launch_act8_unpack(bool bf16, const uint8_t* q, const uint8_t* e, int64_t T, int cols,
                         int fmt, void* out, cudaStream_t s) {
-  const int nvec = cols / 8, slabs = (nvec + kSlab - 1) / kSlab;
-  const unsigned blocks = (unsigned)((T * slabs + 7) / 8);
-  if (bf16)
-    act8_unpack_kernel<uint16_t><<<blocks, 256, 0, s>>>(q, e, T, nvec, slabs, fmt, (uint16_t*)out);
+  if (fmt == kActInt8)
+    bf16 ? unpack<uint16_t, kActInt8>(q, e, T, cols / 8, out, s)
+         : unpack<float, kActInt8>(q, e, T, cols / 8, out, s);
   else
-    act8_unpack_kernel<float><<<blocks, 256, 0, s>>>(q, e, T, nvec, slabs, fmt, (float*)out);
+    bf16 ? unpack<uint16_t, kActE4m3>(q, e, T, cols / 8, out, s)
+         : unpack<float, kActE4m3>(q, e, T, cols / 8, out, s);
 }
 
 cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s) {
-  return bf16 ? norm_fwd<uint16_t>(a, num_sms, s) : norm_fwd<float>(a, num_sms, s);
+  if (!a.q)
+    return bf16 ? norm_fwd<uint16_t, kNoCkpt>(a, num_sms, s) : norm_fwd<float, kNoCkpt>(a, num_sms, s);
+  if (a.fmt == kActInt8)
+    return bf16 ? norm_fwd<uint16_t, kActInt8>(a, num_sms, s)
+                : norm_fwd<float, kActInt8>(a, num_sms, s);
+  return bf16 ? norm_fwd<uint16_t, kActE4m3>(a, num_sms, s) : norm_fwd<float, kActE4m3>(a, num_sms, s);
 }
 
 int64_t norm_part_rows(int64_t T, int d, bool bf16, int num_sms) {
@@ -411,7 +429,10 @@ int64_t norm_part_rows(int64_t T, int d, bool bf16, int num_sms) {
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s) {
-  return bf16 ? norm_bwd<uint16_t>(a, num_sms, s) : norm_bwd<float>(a, num_sms, s);
+  if (a.fmt == kActInt8)
+    return bf16 ? norm_bwd<uint16_t, kActInt8>(a, num_sms, s)
+                : norm_bwd<float, kActInt8>(a, num_sms, s);
+  return bf16 ? norm_bwd<uint16_t, kActE4m3>(a, num_sms, s) : norm_bwd<float, kActE4m3>(a, num_sms, s);
 }
 
 void launch_norm_dgain(const float* part, int64_t rows, int d, bool accumulate, float* out,

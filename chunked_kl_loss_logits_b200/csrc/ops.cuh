@@ -146,12 +146,18 @@ __device__ __forceinline__ float warp_add(float v) {
   return v;
 }
 
-// Bits of the largest magnitude among v (a NaN's bits are above every other's).
-__device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8]) {
+// Bits of the largest magnitude among eight elements (a NaN's bits are above every other's).
+__device__ __forceinline__ uint32_t amax_bits8(const Raw8<float>& r) {
   uint32_t m = 0;
+  const float v[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   return m;
+}
+__device__ __forceinline__ uint32_t amax_bits8(const Raw8<uint16_t>& r) {
+  constexpr uint32_t k = 0x7FFF7FFFu;  // two elements at a time
+  const uint32_t m = __vmaxu2(__vmaxu2(r.u.x & k, r.u.y & k), __vmaxu2(r.u.z & k, r.u.w & k));
+  return max(m << 16, m & 0xFFFF0000u);
 }
 // The same over the four lanes of a block (the whole warp calls it).
 __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
@@ -160,41 +166,44 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
 }
 // Scale byte of a block: 127 = 1.984375 * 2^6 and 448 = 1.75 * 2^8, so the smallest
 // exponent follows from the magnitude's own exponent and fraction bits.
-__device__ __forceinline__ uint32_t act8_scale_byte(uint32_t amax, int fmt) {
+template <int FMT>
+__device__ __forceinline__ uint32_t act8_scale_byte(uint32_t amax) {
   const int ex = (int)(amax >> 23);
   if (ex == 255) return 255u;
   const uint32_t frac = amax & 0x7FFFFFu;
-  const int b = fmt == kActInt8 ? ex - 6 + (frac > 0x7E0000u) : ex - 8 + (frac > 0x600000u);
+  const int b = FMT == kActInt8 ? ex - 6 + (frac > 0x7E0000u) : ex - 8 + (frac > 0x600000u);
   return (uint32_t)max(b, 1);
 }
 // Codes of eight elements under the block's scale byte.
-__device__ __forceinline__ uint2 act8_encode(const float (&v)[8], uint32_t byte, int fmt) {
+template <int FMT>
+__device__ __forceinline__ uint2 act8_encode(const float (&x)[8], uint32_t byte) {
   if (byte == 255u) return make_uint2(0u, 0u);
   const float inv = __uint_as_float((254u - byte) << 23);  // 2^-e
-  float u[8];
+  float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = v[i] * inv;
+  for (int i = 0; i < 8; ++i) v[i] = x[i];
   if (byte >= 247u) {
     // the largest magnitudes of fp32 and bf16 would round up to 2^128: the code below it
-    const float lim = fmt == kActE4m3 ? 240.f : byte >= 249u ? 63.f : 127.f;
+    const float lim = (FMT == kActE4m3 ? 240.f : byte >= 249u ? 63.f : 127.f) *
+                      __uint_as_float(byte << 23);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = fminf(fmaxf(u[i], -lim), lim);
+    for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -lim), lim);
   }
   uint32_t w[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    if (fmt == kActInt8) {
-      // 1.5 * 2^23 + u rounds u to a whole number, whose two's complement is in the low bits
-      // (conversion instructions run at a quarter of the rate)
+    if (FMT == kActInt8) {
+      // 1.5 * 2^23 + x / 2^e is rounded to a whole number, whose two's complement is in the low
+      // bits (conversion instructions run at a quarter of the rate)
       uint32_t c[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(__fadd_rn(u[4 * j + i], 12582912.f));
+      for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(fmaf(v[4 * j + i], inv, 12582912.f));
       w[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     } else {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(u[4 * j], u[4 * j + 1]),
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j] * inv, v[4 * j + 1] * inv),
                                                    __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(u[4 * j + 2], u[4 * j + 3]),
-                                                   __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+          make_float2(v[4 * j + 2] * inv, v[4 * j + 3] * inv), __NV_SATFINITE, __NV_E4M3);
       w[j] = lo | hi << 16;
     }
   }
@@ -203,11 +212,12 @@ __device__ __forceinline__ uint2 act8_encode(const float (&v)[8], uint32_t byte,
 __device__ __forceinline__ float act8_scale(uint32_t byte) {
   return __uint_as_float(byte == 255u ? 0x7FC00000u : byte << 23);
 }
-__device__ __forceinline__ void act8_decode(uint2 q, float scale, int fmt, float (&v)[8]) {
+template <int FMT>
+__device__ __forceinline__ void act8_decode(uint2 q, float scale, float (&v)[8]) {
   const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    if (fmt == kActInt8) {
+    if (FMT == kActInt8) {
       // a code's byte with its sign bit flipped, in the low bits of 2^23, is 2^23 + 128 + code
       const uint32_t x = w[j] ^ 0x80808080u;
 #pragma unroll
