@@ -158,7 +158,7 @@ ckl_status ckl_act8_weight_grad(ckl_handle h, const void* dY, int64_t T, int64_t
           [&] { chk(launch_wgrad(ma, mb, mc, p, h->num_sms, s)); }));
     if (P.n_split > 1)
       chk(L(KID_WGRAD_SUM, 0, 4.0 * n * cols * (P.n_split + 1),
-            [&] { launch_wgrad_sum(out, P.n_split, n * cols, accumulate != 0, dW, s); }));
+            [&] { chk(launch_wgrad_sum(out, P.n_split, n * cols, accumulate != 0, dW, s)); }));
   }
   if ((st = cuda_status(err)) != CKL_OK) return st;
   return wait ? sync_and_read(h, s, nullptr, nullptr) : CKL_OK;
@@ -384,8 +384,8 @@ ckl_status ckl_norm_bwd(ckl_handle h, const void* dY, const void* q, const uint8
   if (err == cudaSuccess) err = set;
   if (err == cudaSuccess)
     err = L(KID_NORM_DGAIN, 0, (double)rows * d * 4,
-            [&] { launch_norm_dgain(a.part, rows, d, accumulate != 0, dgain, s); });
-  return cuda_status(err);
+            [&] { set = launch_norm_dgain(a.part, rows, d, accumulate != 0, dgain, s); });
+  return cuda_status(err != cudaSuccess ? err : set);
 }
 
 }  // extern "C"

@@ -56,6 +56,7 @@ template <typename T, int FMT>
 __global__ void __launch_bounds__(256)
     act8_unpack_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ e, int64_t rows,
                        int nvec, int slabs, T* __restrict__ out) {
+  griddep_launch_dependents();
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int64_t t = w / slabs;
@@ -88,12 +89,13 @@ __global__ void __launch_bounds__(256)
 template <typename T, int WPR, int VPT, bool BWD>
 struct NormCfg {
   static constexpr int kThreads = WPR * 32;
-  // blocks per SM: 24 warps' worth backward (the sums of dg are in registers), 36 forward
-  static constexpr int kWant = (BWD ? 24 : 36) / WPR;
+  // blocks per SM: 24 warps' worth backward (the sums of dg are in registers; two blocks of 16
+  // warps still fit at one vector a lane: 79 us against 91 at d = 4096), 36 forward
+  static constexpr int kWant = (!BWD ? 36 : VPT == 1 && WPR == 16 ? 32 : 24) / WPR;
   static constexpr int kPerSm = kWant < 1 ? 1 : kWant > 16 ? 16 : kWant;
   static constexpr size_t kStage = (size_t)kThreads * VPT * (2 * sizeof(Raw8<T>) + (BWD ? 8 : 0));
   static constexpr size_t kRoom = 200 * 1024 / kPerSm;
-  static constexpr int kDepth = kRoom / kStage >= 4 ? 4 : kRoom / kStage >= 2 ? 2 : 1;
+  static constexpr int kDepth = kRoom / kStage >= 2 ? 2 : 1;
   static constexpr size_t kSmem = kStage * kDepth;
   static_assert(kSmem <= 200 * 1024, "shared memory per block");
 };
@@ -223,13 +225,11 @@ __global__ void __launch_bounds__(WPR * 32, NormCfg<T, WPR, VPT, true>::kPerSm)
         cp_async<8>(qslot(stage, i), a.q + t * a.d + vec(i) * 8);
         if (a.res) copy8(slot(stage, 1, i), (const T*)a.res + t * a.d + vec(i) * 8);
       }
-      // scales and factors are loaded one row ahead, from L2
-      if (lane == 0) prefetch_l2(a.e + t * nb + min(warp * 32 / 4, nb - 1));
-      if (threadIdx.x == 0) prefetch_l2(a.rstd + t);
     }
     cp_async_commit();
   };
   const int64_t step = gridDim.x;
+  griddep_launch_dependents();
 #pragma unroll
   for (int u = 0; u < D; ++u) fetch(blockIdx.x + u * step, u);
   Raw8<T> g[VPT];
@@ -252,34 +252,29 @@ __global__ void __launch_bounds__(WPR * 32, NormCfg<T, WPR, VPT, true>::kPerSm)
     for (int i = 0; i < VPT; ++i)
       next_e[i] = more && vec(i) < nvec ? a.e[(t + step) * nb + (vec(i) >> 2)] : 1u;
     cp_async_wait<D - 1>();
-    Raw8<T> dy[VPT];
-    float h[VPT][8];
+    float ay[VPT][8], h[VPT][8];  // a = dY gain and h of the text above
     float c = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const bool ok = vec(i) < nvec;
-      dy[i] = ok ? *slot(stage, 0, i) : zero8<T>();
-      act8_decode<FMT>(ok ? *qslot(stage, i) : make_uint2(0u, 0u), act8_scale(e[i]), h[i]);
+      act8_decode<FMT>(ok ? *qslot(stage, i) : make_uint2(0u, 0u), act8_scale(e[i]) * rstd, h[i]);
       float d[8], w[8];
-      to_f32(dy[i], d);
+      to_f32(ok ? *slot(stage, 0, i) : zero8<T>(), d);
       to_f32(g[i], w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        h[i][j] *= rstd;
-        const float dh = d[j] * h[i][j];
-        dg[i][j] += dh;
-        c = fmaf(dh, w[j], c);
+        ay[i][j] = d[j] * w[j];
+        dg[i][j] = fmaf(d[j], h[i][j], dg[i][j]);
+        c = fmaf(ay[i][j], h[i][j], c);
       }
     }
     c = row_add<WPR>(c, red[flip], warp, lane) * inv_d;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       if (vec(i) >= nvec) continue;
-      float d[8], w[8];
-      to_f32(dy[i], d);
-      to_f32(g[i], w);
+      float d[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = rstd * (d[j] * w[j] - h[i][j] * c);
+      for (int j = 0; j < 8; ++j) d[j] = rstd * fmaf(-h[i][j], c, ay[i][j]);
       if (a.res) {
         float p[8];
         to_f32(*slot(stage, 1, i), p);
@@ -308,6 +303,7 @@ __global__ void __launch_bounds__(1024)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
   float acc = 0.f;
+  griddep_wait();
   if (c < d) {
 #pragma unroll 8
     for (int64_t r = warp; r < rows; r += 32) acc += part[r * d + c];
@@ -435,9 +431,10 @@ cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, int num_sms, cudaStrea
   return bf16 ? norm_bwd<uint16_t, kActE4m3>(a, num_sms, s) : norm_bwd<float, kActE4m3>(a, num_sms, s);
 }
 
-void launch_norm_dgain(const float* part, int64_t rows, int d, bool accumulate, float* out,
-                       cudaStream_t s) {
-  norm_dgain_kernel<<<(unsigned)((d + 31) / 32), 1024, 0, s>>>(part, rows, d, accumulate, out);
+cudaError_t launch_norm_dgain(const float* part, int64_t rows, int d, bool accumulate, float* out,
+                              cudaStream_t s) {
+  return launch_behind(norm_dgain_kernel, dim3((unsigned)((d + 31) / 32)), 1024, 0, s, part, rows,
+                       d, accumulate, out);
 }
 
 }  // namespace ckl

@@ -66,9 +66,9 @@ struct NormArgs {
 cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s);
 int64_t norm_part_rows(int64_t T, int d, bool bf16, int num_sms);
 cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, int num_sms, cudaStream_t s);
-// out[c] (+)= sum over rows of part[r][c], in a fixed order
-void launch_norm_dgain(const float* part, int64_t rows, int d, bool accumulate, float* out,
-                       cudaStream_t s);
+// out[c] (+)= sum over rows of part[r][c], in a fixed order; behind norm_bwd (launch_behind)
+cudaError_t launch_norm_dgain(const float* part, int64_t rows, int d, bool accumulate, float* out,
+                              cudaStream_t s);
 
 // ---- weight gradient from a checkpoint (k_wgrad.cu)
 struct WgradArgs {
@@ -82,11 +82,12 @@ struct WgradArgs {
 int wgrad_split(int64_t n, int64_t cols, int64_t n_kb, int num_sms);
 // a: the bf16 parts of dY as a (n, T, parts) tensor, boxes of 64 x 64 x 1; b: X' in bf16 as
 // a (cols, T) tensor, boxes of 64 x 64; c: dW or the n_split partial results as an fp32
-// (cols, n, n_split) tensor, boxes of 32 x 32 x 1
+// (cols, n, n_split) tensor, boxes of 32 x 32 x 1. Both this and the sum of the partial results
+// are launched behind the kernel before them (launch_behind).
 cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
                          const WgradArgs& p, int num_sms, cudaStream_t s);
 void launch_split3(const float* x, int64_t n, uint16_t* out, cudaStream_t s);
-void launch_wgrad_sum(const float* part, int n_split, int64_t n, bool add, float* out,
-                      cudaStream_t s);
+cudaError_t launch_wgrad_sum(const float* part, int n_split, int64_t n, bool add, float* out,
+                             cudaStream_t s);
 
 }  // namespace ckl

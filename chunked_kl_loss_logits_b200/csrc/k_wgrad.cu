@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -274,6 +276,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 // up to the value exactly and none overflows; the part of the lowest bits first.
 __global__ void __launch_bounds__(256) split3_kernel(const float* __restrict__ x, int64_t n8,
                                                      uint16_t* __restrict__ out) {
+  griddep_launch_dependents();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n8) return;
   float v[8];
@@ -296,6 +299,7 @@ __global__ void __launch_bounds__(256)
     wgrad_sum_kernel(const float4* __restrict__ part, int n_split, int64_t n4, bool add,
                      float4* __restrict__ out) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  griddep_wait();
   if (i >= n4) return;
   float4 s = part[i];
   for (int k = 1; k < n_split; ++k) {
@@ -335,7 +339,7 @@ cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUten
   cudaError_t e = smem_once(wgrad_kernel, kWgSmem, attr_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -343,6 +347,8 @@ cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUten
   cfg.blockDim = dim3(kWgThreads, 1, 1);
   cfg.dynamicSmemBytes = kWgSmem;
   cfg.stream = s;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // As many pairs as can be resident at once (cached; concurrent first calls agree).
@@ -356,6 +362,7 @@ cudaError_t launch_wgrad(const CUtensorMap& a, const CUtensorMap& b, const CUten
     cached_pairs.store(pairs, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3((unsigned)(2 * std::min(n_tiles, pairs)), 1, 1);
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, wgrad_kernel, a, b, c, p);
 }
 
@@ -363,10 +370,11 @@ void launch_split3(const float* x, int64_t n, uint16_t* out, cudaStream_t s) {
   split3_kernel<<<(unsigned)((n / 8 + 255) / 256), 256, 0, s>>>(x, n / 8, out);
 }
 
-void launch_wgrad_sum(const float* part, int n_split, int64_t n, bool add, float* out,
-                      cudaStream_t s) {
-  wgrad_sum_kernel<<<(unsigned)((n / 4 + 255) / 256), 256, 0, s>>>(
-      reinterpret_cast<const float4*>(part), n_split, n / 4, add, reinterpret_cast<float4*>(out));
+cudaError_t launch_wgrad_sum(const float* part, int n_split, int64_t n, bool add, float* out,
+                             cudaStream_t s) {
+  return launch_behind(wgrad_sum_kernel, dim3((unsigned)((n / 4 + 255) / 256)), 256, 0, s,
+                       reinterpret_cast<const float4*>(part), n_split, n / 4, add,
+                       reinterpret_cast<float4*>(out));
 }
 
 }  // namespace ckl

@@ -128,9 +128,6 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
 // Eight elements by cp.async, and back from there.
 __device__ __forceinline__ void copy8(Raw8<uint16_t>* dst, const uint16_t* src) {
   cp_async<16>(dst, src);
