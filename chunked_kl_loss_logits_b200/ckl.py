@@ -7,8 +7,8 @@ not been built the import of `lib()` raises: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
-import functools
 import os
 import re
 import threading
@@ -224,20 +224,6 @@ ACT8_FORMATS = {"int8": 0, "e4m3": 1}
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)  # the current stream's handle
-
-
-def _on_stream(method):
-    """Adds `stream` to a method of a handle: the call runs, and what it allocates is allocated,
-    on that stream of the handle's device (by default on its current stream)."""
-    @functools.wraps(method)
-    def call(self, *args, stream=None, **kw):
-        if stream is None:
-            return method(self, *args, **kw)
-        if stream.device.index != self._index:
-            raise ValueError("stream must be one of the handle's device")
-        with torch.cuda.stream(stream):
-            return method(self, *args, **kw)
-    return call
 
 
 class Act8:
@@ -558,7 +544,8 @@ class ChunkedKL:
         """t is a dense tensor of the handle's dtype on its device, of this shape if given."""
         if t.dtype is not self.dtype:
             raise TypeError(f"{name} must be {self.dtype}")
-        self._dense(name, t, *shape)
+        if (shape and t.shape != shape) or not t.is_contiguous() or t.get_device() != self._index:
+            self._dense(name, t, *shape)
 
     def _f32(self, name, t, *shape):
         if t.dtype is not torch.float32 or t.shape != shape:
@@ -570,6 +557,14 @@ class ChunkedKL:
             raise ValueError(f"{name} must have the shape {shape}")
         if not t.is_contiguous() or t.get_device() != self._index:
             raise ValueError(f"{name} must be a contiguous tensor on the handle's device")
+
+    @contextlib.contextmanager
+    def _on(self, stream):
+        """The call, and what it allocates, on another stream of the handle's device."""
+        if stream.device.index != self._index:
+            raise ValueError("stream must be one of the handle's device")
+        with torch.cuda.stream(stream):
+            yield
 
     def _ids(self, ids, mask):
         if ids.dtype is not torch.int32:
@@ -613,11 +608,13 @@ class ChunkedKL:
         self._dense("workspace", workspace)
         return workspace
 
-    @_on_stream
     def embed(self, ids, W, mask=None, scale: float = 1.0, V_total: int | None = None, v0: int = 0,
-              out=None, sync: bool = True):
+              out=None, sync: bool = True, stream=None):
         """scale * W[ids - v0] in the handle's dtype (ids' shape, then d): zeros for tokens with
         mask 0 and for ids in [0, V_total) whose row is not among the handle's V (v0 ..)."""
+        if stream is not None:
+            with self._on(stream):
+                return self.embed(ids, W, mask, scale, V_total, v0, out, sync)
         m = self._ids(ids, mask)
         self._rows("W", W, self.V, self.d)
         if out is None:
@@ -630,11 +627,13 @@ class ChunkedKL:
         _check(code, "ckl_embed")
         return out
 
-    @_on_stream
     def embed_vocab_parallel(self, group: VocabGroup, ids, W_shard, mask=None, scale: float = 1.0,
-                             sync: bool = True):
+                             sync: bool = True, stream=None):
         """As embed with W split by vocabulary rows over `group`: the full rows on every rank
         (one all-reduce)."""
+        if stream is not None:
+            with self._on(stream):
+                return self.embed_vocab_parallel(group, ids, W_shard, mask, scale, sync)
         m = self._ids(ids, mask)
         self._rows("W_shard", W_shard, self.V, self.d)
         out = torch.empty(*ids.shape, self.d, dtype=self.dtype, device=self.device)
@@ -650,12 +649,15 @@ class ChunkedKL:
         _check(code, "ckl_embed_vocab_parallel")
         return out
 
-    @_on_stream
     def embed_grad(self, ids, dX, mask=None, scale: float = 1.0, V_total: int | None = None,
                    v0: int = 0, dW=None, accumulate: bool = False, workspace=None,
-                   sync: bool = True):
+                   sync: bool = True, stream=None):
         """dW (V x d, float32) of embed: the given buffer, added to with accumulate=True (a tied
         head's dW from fwd_bwd) and overwritten otherwise, or a new one."""
+        if stream is not None:
+            with self._on(stream):
+                return self.embed_grad(ids, dX, mask, scale, V_total, v0,
+                                       dW, accumulate, workspace, sync)
         m = self._ids(ids, mask)
         self._rows("dX", dX, *ids.shape, self.d)
         if dW is None:
@@ -674,10 +676,12 @@ class ChunkedKL:
         _check(code, "ckl_embed_grad")
         return dW
 
-    @_on_stream
-    def act8_pack(self, x, fmt: str = "int8", out: Act8 | None = None) -> Act8:
+    def act8_pack(self, x, fmt: str = "int8", out: Act8 | None = None, stream=None) -> Act8:
         """The 8-bit checkpoint of x (T x cols, any cols that is a multiple of 8). With `out`, its
         buffers and format are used."""
+        if stream is not None:
+            with self._on(stream):
+                return self.act8_pack(x, fmt, out)
         self._rows("x", x)
         if x.dim() != 2:
             raise ValueError("x must be T x cols")
@@ -692,9 +696,11 @@ class ChunkedKL:
         _check(code, "ckl_act8_pack")
         return out
 
-    @_on_stream
-    def act8_unpack(self, ckpt: Act8, out=None):
+    def act8_unpack(self, ckpt: Act8, out=None, stream=None):
         """The values of a checkpoint (T x cols, the handle's dtype)."""
+        if stream is not None:
+            with self._on(stream):
+                return self.act8_unpack(ckpt, out)
         f = self._ckpt(ckpt)
         T, cols = ckpt.shape
         if out is None:
@@ -706,11 +712,13 @@ class ChunkedKL:
         _check(code, "ckl_act8_unpack")
         return out
 
-    @_on_stream
     def act8_weight_grad(self, dY, ckpt: Act8, dW=None, accumulate: bool = False, workspace=None,
-                         sync: bool = True):
+                         sync: bool = True, stream=None):
         """dW = dY^T X' (n x cols, float32) of a linear layer Y = X W^T with X kept as the
         checkpoint; dY is T x n. dW is added to with accumulate=True."""
+        if stream is not None:
+            with self._on(stream):
+                return self.act8_weight_grad(dY, ckpt, dW, accumulate, workspace, sync)
         f = self._ckpt(ckpt)
         T, cols = ckpt.shape
         self._rows("dY", dY)
@@ -731,13 +739,15 @@ class ChunkedKL:
         _check(code, "ckl_act8_weight_grad")
         return dW
 
-    @_on_stream
     def norm(self, x, gain, residual=None, eps: float = 1e-5, checkpoint: str | None = "int8",
-             out=None):
+             out=None, stream=None):
         """(y, s, checkpoint): s = x + residual (x itself without one), y = s / rms(s) * gain and
         the 8-bit checkpoint of s with the rows' factors, all that norm_bwd needs (None for
         checkpoint=None). out = (y, s, checkpoint): buffers to write to instead of new ones
         (s only with a residual, and it may be x's or residual's)."""
+        if stream is not None:
+            with self._on(stream):
+                return self.norm(x, gain, residual, eps, checkpoint, out)
         T, d = x.shape[0], self.d
         self._rows("x", x, T, d)
         self._rows("gain", gain, d)
@@ -770,12 +780,14 @@ class ChunkedKL:
         _check(code, "ckl_norm")
         return y, s, ckpt
 
-    @_on_stream
     def norm_bwd(self, dY, ckpt: Act8, gain, d_residual=None, dX=None, dgain=None,
-                 accumulate: bool = False, workspace=None):
+                 accumulate: bool = False, workspace=None, stream=None):
         """(dX, dgain) of norm from its checkpoint: dX (T x d) is the gradient of x and of
         residual, d_residual the gradient that reaches s other than through y; dgain (d,
         float32) is added to with accumulate=True."""
+        if stream is not None:
+            with self._on(stream):
+                return self.norm_bwd(dY, ckpt, gain, d_residual, dX, dgain, accumulate, workspace)
         T, d = ckpt.shape[0], self.d
         f = self._ckpt(ckpt, None, d)
         if ckpt._ptrs[2] is None:
@@ -912,13 +924,18 @@ _OP_HANDLES = threading.local()  # a handle must not be used by two calls at onc
 def operator_handle(t, V: int = 1) -> ChunkedKL:
     """The calling thread's cached handle for t's device and dtype, with d = t's last dimension
     and V rows of W: for the calls that need no teacher cache (embed, act8_*, norm*)."""
-    if t.device.type != "cuda":
+    index = t.get_device()
+    if index < 0:
         raise ValueError("inputs must be CUDA tensors")
-    cache = _OP_HANDLES.__dict__.setdefault("handles", {})
-    key = (t.device.index, t.dtype, V, t.shape[-1])
-    h = cache.get(key)
-    if h is None:
-        h = cache[key] = ChunkedKL(V, t.shape[-1], 1, dtype=t.dtype, max_chunk=1, device=t.device)
+    d = t.shape[-1]
+    key = (index, t.dtype, V, d)
+    try:
+        return _OP_HANDLES.handles[key]
+    except AttributeError:
+        _OP_HANDLES.handles = {}
+    except KeyError:
+        pass
+    h = _OP_HANDLES.handles[key] = ChunkedKL(V, d, 1, dtype=t.dtype, max_chunk=1, device=t.device)
     return h
 
 
