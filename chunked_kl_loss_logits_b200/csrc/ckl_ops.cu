@@ -66,23 +66,30 @@ ckl_status check_act8(const ckl_ctx* h, int64_t T, int64_t cols, int fmt, const 
   return CKL_OK;
 }
 
+// The contraction runs over `chunk` tokens at a time, so that the bf16 copy of the checkpoint
+// stays below kWgradChunkBytes whatever T is. (Chunks small enough to stay in L2, each unpacked
+// behind the contraction of the one before, measured slower: 32768 x 2880 x 2880 in one chunk 586 us,
+// in chunks of 96 MB 603, of 48 MB 616: every contraction has its own start and end.)
 struct WgradPlan {
-  int64_t parts = 0, kb_part = 0, n_kb = 0, kb_split = 0;
+  int64_t chunk = 0, parts = 0;
   int n_split = 1;
   size_t off_x = 0, off_parts = 0, off_sum = 0, total = 0;
 };
 
+constexpr int64_t kWgradChunkBytes = 256 << 20;  // of the bf16 copy
+constexpr int64_t kWgradChunkStep = 4096;        // tokens: whole accumulator ranges of the kernel
+
 WgradPlan wgrad_plan(const ckl_ctx* h, int64_t T, int64_t n, int64_t cols) {
   WgradPlan p;
   p.parts = h->dtype == CKL_BF16 ? 1 : 3;
-  p.kb_part = (T + 63) / 64;
-  p.n_kb = p.parts * p.kb_part;
-  p.n_split = p.n_kb ? wgrad_split(n, cols, p.n_kb, h->num_sms) : 1;
-  p.kb_split = (p.n_kb + p.n_split - 1) / p.n_split;
+  const int64_t fit = kWgradChunkBytes / (cols * 2) / kWgradChunkStep * kWgradChunkStep;
+  p.chunk = std::max<int64_t>(1, std::min(T, std::max(fit, kWgradChunkStep)));
+  p.n_split = wgrad_split(n, cols, p.parts * ((p.chunk + 63) / 64), h->num_sms);
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
-  p.off_x = take((size_t)T * cols * 2);
-  if (p.parts > 1) p.off_parts = take((size_t)T * n * 2 * p.parts);
+  if (T == 0) return p;
+  p.off_x = take((size_t)p.chunk * cols * 2);
+  if (p.parts > 1) p.off_parts = take((size_t)p.chunk * n * 2 * p.parts);
   if (p.n_split > 1) p.off_sum = take((size_t)p.n_split * n * cols * 4);
   p.total = o;
   return p;
@@ -131,34 +138,46 @@ ckl_status ckl_act8_weight_grad(ckl_handle h, const void* dY, int64_t T, int64_t
   } else {
     unsigned char* base = static_cast<unsigned char*>(workspace);
     Launcher L{h, s};
-    const void* a = dY;
-    if (P.parts > 1) {
-      uint16_t* parts = reinterpret_cast<uint16_t*>(base + P.off_parts);
-      chk(L(KID_WGRAD_PARTS, 0, (double)T * n * 10,
-            [&] { launch_split3(static_cast<const float*>(dY), T * n, parts, s); }));
-      a = parts;
-    }
-    void* x = base + P.off_x;
-    chk(L(KID_ACT8_UNPACK, 0, (double)T * cols * (2.0 + 33.0 / 32), [&] {
-      launch_act8_unpack(true, static_cast<const uint8_t*>(q), scale, T, (int)cols, fmt, x, s);
-    }));
+    const size_t es = elem(h);
+    const int nb = (int)((cols + 31) / 32);
     float* out = P.n_split > 1 ? reinterpret_cast<float*>(base + P.off_sum) : dW;
-    CUtensorMap ma, mb, mc;
-    if (!make_map_planes(h, &ma, a, n, T, P.parts, 64) ||
-        !make_map(h, &mb, x, cols, T, (uint64_t)cols * 2, 64, 64) ||
-        !make_map_planes(h, &mc, out, cols, n, P.n_split, 32, true))
-      return CKL_ERR_CUDA;
-    WgradArgs p{};
-    p.n = (int)n; p.cols = (int)cols;
-    p.kb_part = (int)P.kb_part; p.n_kb = (int)P.n_kb;
-    p.n_split = P.n_split; p.kb_split = (int)P.kb_split;
-    p.add = P.n_split == 1 && accumulate;
-    p.status = h->d_status;
-    chk(L(KID_WGRAD, 2.0 * T * n * cols, 0,
-          [&] { chk(launch_wgrad(ma, mb, mc, p, h->num_sms, s)); }));
-    if (P.n_split > 1)
-      chk(L(KID_WGRAD_SUM, 0, 4.0 * n * cols * (P.n_split + 1),
-            [&] { chk(launch_wgrad_sum(out, P.n_split, n * cols, accumulate != 0, dW, s)); }));
+    void* x = base + P.off_x;
+    for (int64_t t0 = 0; t0 < T && err == cudaSuccess; t0 += P.chunk) {
+      const int64_t Tc = std::min(P.chunk, T - t0);
+      const bool add = accumulate || t0 > 0;
+      const void* a = static_cast<const unsigned char*>(dY) + (size_t)(t0 * n) * es;
+      chk(L(KID_ACT8_UNPACK, 0, (double)Tc * cols * (2.0 + 33.0 / 32), [&] {
+        launch_act8_unpack(true, static_cast<const uint8_t*>(q) + t0 * cols, scale + t0 * nb, Tc,
+                           (int)cols, fmt, x, s);
+      }));
+      if (P.parts > 1) {
+        uint16_t* parts = reinterpret_cast<uint16_t*>(base + P.off_parts);
+        chk(L(KID_WGRAD_PARTS, 0, (double)Tc * n * 10,
+              [&] { launch_split3(static_cast<const float*>(a), Tc * n, parts, s); }));
+        a = parts;
+      }
+      CUtensorMap ma, mb, mc;
+      if (!make_map_planes(h, &ma, a, n, Tc, P.parts, 64) ||
+          !make_map(h, &mb, x, cols, Tc, (uint64_t)cols * 2, 64, 64) ||
+          !make_map_planes(h, &mc, out, cols, n, P.n_split, 32, true))
+        return CKL_ERR_CUDA;
+      WgradArgs p{};
+      p.n = (int)n; p.cols = (int)cols;
+      p.kb_part = (int)((Tc + 63) / 64);
+      p.n_kb = (int)P.parts * p.kb_part;
+      // a short last chunk takes as many of the ranges as it has steps for
+      const int range = (p.n_kb + P.n_split - 1) / P.n_split;
+      p.n_split = (p.n_kb + range - 1) / range;
+      p.kb_split = range;
+      p.add = P.n_split == 1 && add;
+      p.status = h->d_status;
+      chk(L(KID_WGRAD, 2.0 * Tc * n * cols, 0,
+            [&] { chk(launch_wgrad(ma, mb, mc, p, h->num_sms, s)); }));
+      if (P.n_split > 1)
+        chk(L(KID_WGRAD_SUM, 0, 4.0 * n * cols * (p.n_split + 1), [&] {
+          chk(launch_wgrad_sum(out, p.n_split, n * cols, add, dW, s));
+        }));
+    }
   }
   if ((st = cuda_status(err)) != CKL_OK) return st;
   return wait ? sync_and_read(h, s, nullptr, nullptr) : CKL_OK;

@@ -49,6 +49,7 @@ constexpr int kFlush = 64;                    // steps (of 64 tokens) one accumu
 constexpr int kBox = 32 * 128;                // a staged 32 x 32 fp32 box of an epilogue warp
 constexpr int kWgSmem = 1024 + kStages * kStageBytes + 4 * 2 * kBox + 256;
 static_assert(kWgSmem <= 232448, "shared memory per CTA");
+constexpr long long kPaceMax = 1LL << 22;     // SM cycles; bounds the measured time between sums
 constexpr uint16_t kPair = 0x3;
 
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m,
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     const int q = warp & 3;  // TMEM lane quarter this warp may access
     unsigned char* mine = boxes + q * 2 * kBox;
     int it = 0, filled = 0;
+    long long t_prev = 0;
     bool ok = true;
     for (int tile = pair; ok && tile < n_tiles; tile += n_pairs) {
       const WgTile c = wg_tile(p, n_m, n_n, tile);
@@ -229,6 +231,13 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           break;
         }
         tc_fence_after();
+        // The sums of all pairs are ready at about the same moment. So that their additions do not
+        // fill L2 just when the next operands are wanted, box group cc leaves cc / 10 of the time
+        // between two sums later, where another sum follows.
+        const long long t_now = clock64();
+        const bool more = kf + kFlush < c.kb1 || tile + n_pairs < n_tiles;
+        const long long gap = t_prev > 0 && more ? min(t_now - t_prev, kPaceMax) / 10 : 0;
+        t_prev = t_now;
         const bool add = p.add || kf > c.kb0;
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kAccCols);
         // this tile's earlier sum is in place: additions to an element keep their order
@@ -237,6 +246,10 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         for (int cc = 0; cc < kBN / 32; ++cc) {
           const int cb = c.nt * kBN + cc * 32;
           if (cb >= p.cols || row0 >= p.n) break;
+          if (gap > 0) {
+            const long long due = t_now + gap * cc;
+            while (clock64() < due) __nanosleep(128);
+          }
           float v[32];
           tmem_ld32(taddr + cc * 32, v);
           unsigned char* box = mine + (filled++ & 1) * kBox;

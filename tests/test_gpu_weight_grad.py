@@ -77,6 +77,23 @@ def test_against_the_oracle_and_exact_sums():
             assert torch.equal(got.double(), dY.double().t() @ x.double())
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_more_tokens_than_one_chunk(dt):
+    """50001 tokens of 2880 columns are contracted in two chunks; small integers, so that every
+    order of the sums is exact."""
+    T, n, cols = 50001, 72, 2880
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randint(-8, 9, (T, cols), generator=g, device="cuda").to(DT[dt])
+    dY = torch.randint(-4, 5, (T, n), generator=g, device="cuda").to(DT[dt])
+    h = ckl.operator_handle(dY)
+    ckpt = h.act8_pack(x)
+    want = dY.double().t() @ x.double()
+    assert torch.equal(h.act8_weight_grad(dY, ckpt).double(), want)
+    base = torch.randint(-99, 99, (n, cols), generator=g, device="cuda").float()
+    got = h.act8_weight_grad(dY, ckpt, dW=base.clone(), accumulate=True)
+    assert torch.equal(got.double(), want + base.double())
+
+
 def test_fp32_gradients_keep_all_their_bits():
     """One token: the product of a 24-bit dY and a code, rounded to fp32."""
     g = torch.Generator(device="cuda").manual_seed(1)
