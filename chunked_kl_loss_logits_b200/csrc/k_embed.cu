@@ -22,10 +22,10 @@ namespace {
 
 // A token's row among those held here, or V (mask 0, another rank's row, or out of range).
 __device__ __forceinline__ int32_t row_of(const EmbedIds& a, int32_t id, uint8_t keep, bool& bad) {
-  const int32_t r = id - a.v0;
   const bool in = id >= 0 && id < a.V_total;
   bad |= keep && !in;
-  return keep && in && r >= 0 && r < a.V ? r : a.V;
+  const int32_t r = keep && in ? id - a.v0 : -1;
+  return r >= 0 && r < a.V ? r : a.V;
 }
 
 // One warp per (token, 128 vectors of 8 columns).

@@ -107,6 +107,26 @@ def test_embed_grad_many_tokens_three_digits():
     assert torch.equal(h.embed_grad(ids, dX).double(), want)
 
 
+def test_embed_grad_largest_keys():
+    """A vocabulary of 28 bits (four digits) and a shard of it that starts far up."""
+    V, d = 140_000_000, 8
+    ids = torch.tensor([V - 1, 0, V - 1, 77_777_777, 0, V - 1], dtype=torch.int32, device="cuda")
+    dX = torch.arange(48, device="cuda", dtype=torch.float32).view(6, 8)
+    h = ckl.ChunkedKL(V, d, 1, dtype=torch.float32, max_chunk=1)
+    dW = h.embed_grad(ids, dX)
+    assert torch.equal(dW[V - 1], dX[0] + dX[2] + dX[5]) and torch.equal(dW[0], dX[1] + dX[4])
+    assert torch.equal(dW[77_777_777], dX[3])
+    dW[V - 1] = dW[0] = dW[77_777_777] = 0
+    assert not dW.any()
+    h.close()
+    s = ckl.operator_handle(dX, V=10)
+    got = s.embed_grad(ids, dX, V_total=2 ** 31 - 1, v0=77_777_770)
+    assert torch.equal(got[7], dX[3]) and not got[:7].any() and not got[8:].any()
+    wild = torch.tensor([-2 ** 31, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    with pytest.raises(ckl.CKLError):
+        s.embed_grad(wild, dX[:2], V_total=2 ** 31 - 1, v0=77_777_770)
+
+
 def test_masks_and_lengths_that_leave_nothing():
     ids, _, W, dX = case(40, 64, 30, "bf16")
     h = ckl.operator_handle(W, V=30)
@@ -219,6 +239,22 @@ def test_calls_captured_in_a_graph_and_on_a_stream():
         torch.cuda.synchronize()
         assert torch.equal(out, h.embed(ids, W, mask=mask))
         assert torch.equal(dW, h.embed_grad(ids, dX, mask=mask))
+
+
+def test_two_calls_in_flight_and_a_stream_of_its_own():
+    cs = [case(5000, 264, 3000, "bf16", seed=k, hot=0.2) for k in (0, 1)]
+    hs = [ckl.ChunkedKL(3000, 264, 1, max_chunk=1) for _ in cs]
+    alone = [(h.embed(c[0], c[2]), h.embed_grad(c[0], c[3])) for h, c in zip(hs, cs)]
+    torch.cuda.synchronize()
+    ss = [torch.cuda.Stream() for _ in cs]
+    for _ in range(5):
+        both = [(h.embed(c[0], c[2], sync=False, stream=s), h.embed_grad(c[0], c[3], sync=False, stream=s))
+                for h, c, s in zip(hs, cs, ss)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    [h.sync_status() for h in hs]
+    [h.close() for h in hs]
 
 
 def test_autograd_embedding():
