@@ -23,6 +23,9 @@ namespace {
 constexpr int kNoCkpt = -1;
 constexpr int kSlab = 128;  // vectors of eight columns a warp handles of one row (pack, unpack)
 
+// One warp for 128 vectors of a row, four in flight per lane; four lanes make an 8-bit block.
+// Bound by memory: 32768 x 2880 bf16, pack 50 us (5.7 TB/s), unpack 46 us (6.2 TB/s), where a copy
+// runs at 6.1. Codes by conversion instructions instead of one fused operation: 59 us.
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256)
     act8_pack_kernel(const T* __restrict__ X, int64_t rows, int nvec, int slabs,
@@ -85,7 +88,12 @@ __global__ void __launch_bounds__(256)
 
 // The norm kernels: a block of WPR warps walks rows in steps of the grid, each lane with VPT
 // vectors of eight columns. What it needs of the rows ahead is on its way to shared memory
-// (cp.async, each thread its own vectors, so that nothing but the row sum is synchronised).
+// (cp.async, each thread its own vectors, so that nothing but the row sum is synchronised): two
+// rows, as four keep fewer blocks on an SM (272 us against 275 for both passes below).
+// 32768 x 2880 bf16 with a residual: forward 148 us (5.75 TB/s), backward 121 us (5.5 TB/s). Rows in
+// registers alone, several to a block, took 173 and 215 us: the sums of dg leave room for too few
+// warps to keep HBM busy without copies under way. Asking L2 for the scales of the rows ahead
+// cost 8 us.
 template <typename T, int WPR, int VPT, bool BWD>
 struct NormCfg {
   static constexpr int kThreads = WPR * 32;
@@ -297,8 +305,7 @@ __global__ void __launch_bounds__(WPR * 32, NormCfg<T, WPR, VPT, true>::kPerSm)
 
 // 32 columns per block; each of 32 warps adds every 32nd line, then the warps' sums in order.
 __global__ void __launch_bounds__(1024)
-    norm_dgain_kernel(const float* __restrict__ part, int64_t rows, int d, bool accumulate,
-                      float* __restrict__ out) {
+    norm_dgain_kernel(const float* part, int64_t rows, int d, bool accumulate, float* out) {
   __shared__ float red[32][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;

@@ -66,7 +66,9 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedIds a, const T* _
 // Stable least-significant-digit radix sort by one cluster of CTAs. Each of the cluster's
 // warps owns a contiguous range of the items, so "count per (digit, warp), prefix over
 // digits, then over warps" gives every item its place, and equal keys keep their order.
-// The digit counts of the other CTAs are read from their shared memory.
+// The digit counts of the other CTAs are read from their shared memory. 32768 tokens, 18-bit
+// keys in two digits: 14 us, a chain of latencies (cluster barriers, counts of the others, the
+// scattered stores) rather than work; 16 CTAs instead of 8 take a tenth less.
 constexpr int kSortWarps = 32;
 constexpr int kBatch = 4;
 constexpr int kMaxDigitBits = 9;
@@ -222,7 +224,8 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
 __device__ __forceinline__ int32_t key_of(uint64_t it) { return (int32_t)(it >> 32); }
 
 // dst (+)= scale * v. The addition is made in L2, so that the thread does not wait for the old
-// value; a call adds to an element once, so it is the sum of two numbers either way.
+// value (121 us against 125 for the call at 32768 x 2880); a call adds to an element once, so it is
+// the sum of two numbers either way (an L2 addition takes subnormal numbers for zero).
 __device__ __forceinline__ void add_row8(float* dst, const float (&v)[8], float scale,
                                          bool accumulate) {
   float o[8];
@@ -245,15 +248,17 @@ __device__ __forceinline__ void add_row8(float* dst, const float (&v)[8], float 
 // each group's share goes to shared memory, and the group in which the row begins adds the
 // shares up in order; of a row that spans tiles the tile's sum goes to part: slot 0 where the
 // row began in an earlier tile, slot 1 where it begins here.
-constexpr int kHead = 1, kTail = 2, kThrough = 4;  // a share of a row that began before, that goes on, both
-
-constexpr int kAhead = 4;                         // rows of dX loaded at a time
+// 32768 tokens of 2880 columns, 13 thousand different ids of 201088: 90 us, 5.5 TB/s; 8 rows of
+// dX ahead instead of 4 (fewer CTAs an SM) 140 us, 5 CTAs an SM (spills) 110 us.
+constexpr int kHead = 1, kTail = 2;  // flags of a group: a share of a row that began before; a row begins, goes on
+constexpr int kThrough = 4;          // with kHead: the row also goes on
+constexpr int kAhead = 4;            // rows of dX loaded at a time
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-    embed_grad_kernel(const uint64_t* __restrict__ sorted, int64_t n, int32_t V,
+    embed_grad_kernel(const uint64_t* sorted, int64_t n, int32_t V,
                       const T* __restrict__ dX, int nvec, EmbedShape shape, float scale,
-                      bool accumulate, float* __restrict__ dW, float* __restrict__ part) {
+                      bool accumulate, float* dW, float* part) {
   __shared__ float4 head_sum[256][2];
   __shared__ int flags[256];
   const int lanes = shape.lanes, groups = 256 / lanes;
@@ -359,9 +364,8 @@ __global__ void __launch_bounds__(256)
 // up the row's partial sums, each of the eight warps a contiguous share of them, then the
 // eight in order.
 __global__ void __launch_bounds__(256)
-    embed_join_kernel(const uint64_t* __restrict__ sorted, int64_t n, int32_t V, int d, int tile_n,
-                      float scale, bool accumulate, float* __restrict__ dW,
-                      const float* __restrict__ part) {
+    embed_join_kernel(const uint64_t* sorted, int64_t n, int32_t V, int d, int tile_n, float scale,
+                      bool accumulate, float* dW, const float* part) {
   __shared__ float4 red[8][32][2];
   const int64_t tile = blockIdx.x, i0 = tile * tile_n, i1 = i0 + tile_n;
   griddep_wait();

@@ -309,8 +309,7 @@ __global__ void __launch_bounds__(256) split3_kernel(const float* __restrict__ x
 
 // out (+)= the sum of n_split partial results, in order.
 __global__ void __launch_bounds__(256)
-    wgrad_sum_kernel(const float4* __restrict__ part, int n_split, int64_t n4, bool add,
-                     float4* __restrict__ out) {
+    wgrad_sum_kernel(const float4* part, int n_split, int64_t n4, bool add, float4* out) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   griddep_wait();
   if (i >= n4) return;

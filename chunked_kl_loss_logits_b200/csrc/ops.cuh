@@ -37,7 +37,8 @@ cudaError_t smem_once(F* fn, size_t bytes, std::atomic<uint64_t>& set) {
 }
 
 // Launch behind the kernel just enqueued on s, which it may overlap up to its griddep_wait(): the
-// kernel calls that before it touches what the one before wrote or reads what that may write.
+// kernel calls that before it touches what the one before wrote or reads what that may write (and
+// takes no such pointer as const __restrict__: its loads are not read-only for the kernel's life).
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*fn)(P...), dim3 grid, unsigned threads, size_t smem,
                           cudaStream_t s, A... args) {

@@ -311,9 +311,12 @@ ckl_status ckl_embed_vocab_parallel(ckl_handle h, const ckl_vocab_group* group, 
  * dX: T x d, the handle's dtype. dW: V x d fp32. accumulate != 0 adds to dW, for example to
  * the dW that ckl_fwd_bwd wrote for a tied head, and leaves the rows of ids that do not
  * occur as they are; otherwise dW is overwritten (zeros where no token falls). A row's sum is
- * formed in fp32 in order of position and multiplied by scale once. Tokens with mask 0, ids of
+ * formed in fp32 in a fixed order and multiplied by scale once (the addition to an old value
+ * takes subnormal numbers for zero). Tokens with mask 0, ids of
  * other ranks' rows and ids outside [0, V_total) (status CKL_ERR_INDEX_RANGE) add nothing.
- * Workspace: ckl_embed_grad_workspace_bytes, O(T): 16 T bytes and at most 2 T d. */
+ * Workspace: ckl_embed_grad_workspace_bytes, O(T): 16 T bytes and a few per cent of dX. A
+ * workspace serves one call at a time, here and below: two captured graphs that may run at once
+ * need one each. */
 ckl_status ckl_embed_grad_workspace_bytes(ckl_handle h, int64_t T, size_t* bytes);
 ckl_status ckl_embed_grad(ckl_handle h, const int32_t* ids, const uint8_t* mask, const void* dX,
                           int64_t T, int64_t V_total, int64_t v0, float scale, int accumulate,
