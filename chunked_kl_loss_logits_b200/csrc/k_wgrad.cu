@@ -13,13 +13,15 @@
 // Work unit: a 256 x 256 tile of dW and a range of tokens, by a CTA pair
 // (tcgen05.mma.cta_group::2), 64 tokens a step. Both operands are MN-major as they lie in
 // memory, and come by TMA. The tensor cores cut the running sum at each step instead of
-// rounding it: a relative error that grows with the number of steps (1e-6 at 2048 tokens,
-// 1.5e-5 at 32768). So a tile's sum is taken out after kFlush steps and added up in fp32 by
-// the epilogue; the parts of an fp32 dY are contracted smallest first, which keeps their
-// errors as small as they are. Roles, per CTA (192 threads):
+// rounding it: a relative error that grows with the number of steps (1.2e-6 at 2048 tokens, 3e-5
+// at 32768). So an accumulator sums kFlush steps only, and the epilogue warps, whose registers
+// hold the CTA's 128 x 256 share of the tile, add it up there in fp32 while the MMAs fill
+// the other accumulator. (Adding to dW in L2 instead costs 25 us every 64 steps at 32768 x 2880 x
+// 2880.) The parts of an fp32 dY are contracted smallest first, which keeps their errors as
+// small as they are. Roles, per CTA (320 threads):
 //   warp 0      TMA producer (both CTAs; completion on the even CTA's `full`)
 //   warp 1      allocates TMEM; in the even CTA one thread issues the MMAs
-//   warps 2..5  epilogue: the CTA's 128 accumulator rows, while the MMAs fill the other one
+//   warps 2..9  epilogue: 32 accumulator rows by 128 columns each
 // Every wait is bounded (common.cuh).
 //
 // Converting the codes inside the contraction (by further warps, from the codes in shared
@@ -43,13 +45,13 @@ constexpr int kBN = 256, kBNH = kBN / 2;      // X' columns of the pair, of a CT
 constexpr int kStages = 6;
 constexpr int kAtom = 64 * 128;               // 64 (MN) x 64 (K) bf16
 constexpr int kABytes = 2 * kAtom, kBBytes = 2 * kAtom, kStageBytes = kABytes + kBBytes;
-constexpr int kWgThreads = 192;
+constexpr int kEpiWarps = 8;                  // two per lane quarter of TMEM, 128 columns each
+constexpr int kWgThreads = (2 + kEpiWarps) * 32;
 constexpr int kTmemCols = 512, kAccCols = 256;
-constexpr int kFlush = 64;                    // steps (of 64 tokens) one accumulator sums
+constexpr int kFlush = 16;                    // steps (of 64 tokens) one accumulator sums
 constexpr int kBox = 32 * 128;                // a staged 32 x 32 fp32 box of an epilogue warp
-constexpr int kWgSmem = 1024 + kStages * kStageBytes + 4 * 2 * kBox + 256;
+constexpr int kWgSmem = 1024 + kStages * kStageBytes + kEpiWarps * kBox + 256;
 static_assert(kWgSmem <= 232448, "shared memory per CTA");
-constexpr long long kPaceMax = 1LL << 22;     // SM cycles; bounds the measured time between sums
 constexpr uint16_t kPair = 0x3;
 
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m,
@@ -78,6 +80,22 @@ __device__ __forceinline__ void tma_put_3d(const CUtensorMap* m, const void* src
         : "memory");
 }
 
+// sum += 16 consecutive f32 columns of this thread's TMEM lane (warp-collective).
+__device__ __forceinline__ void tmem_add16(uint32_t taddr, float* sum) {
+  uint32_t r[16];
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sum[i] += __uint_as_float(r[i]);
+}
+
 struct WgTile {
   int mt, nt, split, kb0, kb1;
 };
@@ -98,8 +116,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  unsigned char* boxes = smem + kStages * kStageBytes;  // [4 warps][2]
-  uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 4 * 2 * kBox);  // even CTA's in use
+  unsigned char* boxes = smem + kStages * kStageBytes;  // one for each epilogue warp
+  uint64_t* full = reinterpret_cast<uint64_t*>(boxes + kEpiWarps * kBox);  // even CTA's in use
   uint64_t* empty = full + kStages;     // both CTAs
   uint64_t* tfull = empty + kStages;    // [2] both CTAs
   uint64_t* tempty = tfull + 2;         // [2] even CTA's in use
@@ -120,7 +138,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * 4);
+      mbar_init(&tempty[b], 2 * kEpiWarps);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -216,14 +234,18 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;  // TMEM lane quarter this warp may access
-    unsigned char* mine = boxes + q * 2 * kBox;
-    int it = 0, filled = 0;
-    long long t_prev = 0;
+    const int q = warp & 3;           // TMEM lane quarter this warp may access
+    const int half = (warp - 2) >> 2;  // its 128 of the accumulator's 256 columns
+    unsigned char* box = boxes + (warp - 2) * kBox;
+    int it = 0;
     bool ok = true;
     for (int tile = pair; ok && tile < n_tiles; tile += n_pairs) {
       const WgTile c = wg_tile(p, n_m, n_n, tile);
       const int row0 = c.mt * 2 * kBM + (int)rank * kBM + q * 32;  // this warp's rows of dW
+      const int col0 = c.nt * kBN + half * 128;
+      float sum[128];  // this thread's row: the accumulators taken out so far
+#pragma unroll
+      for (int j = 0; j < 128; ++j) sum[j] = 0.f;
       for (int kf = c.kb0; kf < c.kb1; kf += kFlush, ++it) {
         const int buf = it & 1;
         if (!mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, p.status)) {
@@ -231,46 +253,33 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           break;
         }
         tc_fence_after();
-        // The sums of all pairs are ready at about the same moment. So that their additions do not
-        // fill L2 just when the next operands are wanted, box group cc leaves cc / 10 of the time
-        // between two sums later, where another sum follows.
-        const long long t_now = clock64();
-        const bool more = kf + kFlush < c.kb1 || tile + n_pairs < n_tiles;
-        const long long gap = t_prev > 0 && more ? min(t_now - t_prev, kPaceMax) / 10 : 0;
-        t_prev = t_now;
-        const bool add = p.add || kf > c.kb0;
-        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kAccCols);
-        // this tile's earlier sum is in place: additions to an element keep their order
-        if (lane == 0) bulk_wait_all();
-#pragma unroll 1
-        for (int cc = 0; cc < kBN / 32; ++cc) {
-          const int cb = c.nt * kBN + cc * 32;
-          if (cb >= p.cols || row0 >= p.n) break;
-          if (gap > 0) {
-            const long long due = t_now + gap * cc;
-            while (clock64() < due) __nanosleep(128);
-          }
-          float v[32];
-          tmem_ld32(taddr + cc * 32, v);
-          unsigned char* box = mine + (filled++ & 1) * kBox;
-          if (lane == 0) bulk_wait_read<1>();  // the box's previous contents have been read
+        const uint32_t taddr =
+            tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kAccCols + half * 128);
+#pragma unroll
+        for (int cc = 0; cc < 8; ++cc) tmem_add16(taddr + cc * 16, &sum[cc * 16]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_map(&tempty[buf], 0));
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        if (col0 + cc * 32 < p.cols && row0 < p.n) {
+          if (lane == 0) bulk_wait_read<0>();  // the box's previous contents have been read
           __syncwarp();
           uint4* rowp = reinterpret_cast<uint4*>(box + lane * 128);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            rowp[j ^ (lane & 7)] = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                              __float_as_uint(v[4 * j + 2]),
-                                              __float_as_uint(v[4 * j + 3]));
+            rowp[j ^ (lane & 7)] = make_uint4(
+                __float_as_uint(sum[cc * 32 + 4 * j]), __float_as_uint(sum[cc * 32 + 4 * j + 1]),
+                __float_as_uint(sum[cc * 32 + 4 * j + 2]), __float_as_uint(sum[cc * 32 + 4 * j + 3]));
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_put_3d(&tmC, box, cb, row0, c.split, add);
+            tma_put_3d(&tmC, box, col0 + cc * 32, row0, c.split, p.add);
             bulk_commit();
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_map(&tempty[buf], 0));
       }
     }
     if (lane == 0) bulk_wait_all();
