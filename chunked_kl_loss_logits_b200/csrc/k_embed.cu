@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
         if (ib + j * 32 + lane < i1) atomicAdd(&myhist[digit(it[j])], 1u);
     }
     __syncthreads();
-    uint32_t mine = 0;
     if (tid < bins) {
+      uint32_t mine = 0;
 #pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t c = hist[w * bins + tid];
@@ -188,11 +188,8 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    if (tid < bins) {
-      uint32_t pre = 0;
-      for (int w = 0; w < warp; ++w) pre += wsum[w];
-      base[tid] = pre + incl - all + before;
-    }
+    const uint32_t pre = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u);
+    if (tid < bins) base[tid] = pre + incl - all + before;
     __syncthreads();
 #pragma unroll 1
     for (int64_t ib = i0; ib < i1; ib += kBatch * 32) {
@@ -368,24 +365,25 @@ __global__ void __launch_bounds__(256)
                       bool accumulate, float* dW, const float* part) {
   __shared__ float4 red[8][32][2];
   const int64_t tile = blockIdx.x, i0 = tile * tile_n, i1 = i0 + tile_n;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
   if (i1 >= n) return;
-  const int32_t cur = key_of(sorted[i1 - 1]);
-  if (cur == V || key_of(sorted[i1]) != cur) return;
-  if (key_of(sorted[i0]) == cur && i0 > 0 && key_of(sorted[i0 - 1]) == cur) return;
-  // the tiles after this one that begin with the row: doubling the step, then halving it
-  auto goes_on = [&](int64_t k) {
-    return (tile + k) * tile_n < n && key_of(sorted[(tile + k) * tile_n]) == cur;
+  // the first keys of the 32 tiles after this one, a lane each, beside those that tell whether a
+  // row begins here and goes on: one round of loads
+  auto first_key = [&](int64_t k) {
+    return (tile + k) * tile_n < n ? key_of(sorted[(tile + k) * tile_n]) : -1;
   };
-  int64_t lo = 1, step = 1;  // tile + lo begins with the row
-  while (goes_on(lo + step)) {
-    lo += step;
-    step *= 2;
+  int32_t ahead = first_key(1 + lane);
+  const int32_t cur = key_of(sorted[i1 - 1]), first = key_of(sorted[i0]);
+  const int32_t before = i0 > 0 ? key_of(sorted[i0 - 1]) : -1;
+  unsigned same = __ballot_sync(0xffffffffu, ahead == cur);
+  if (cur == V || !(same & 1u) || (first == cur && before == cur)) return;
+  int64_t n_part = 1;  // slot 1 of this tile, slot 0 of the tiles that begin with the row
+  while (same == 0xffffffffu) {
+    n_part += 32;
+    same = __ballot_sync(0xffffffffu, first_key(n_part + lane) == cur);
   }
-  for (; step > 1; step /= 2)
-    if (goes_on(lo + step / 2)) lo += step / 2;
-  const int64_t n_part = lo + 1;  // slot 1 of this tile, slot 0 of the others
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  n_part += __ffs(~same) - 1;
   const int64_t share = (n_part + 7) / 8;
   const int64_t p0 = min(n_part, warp * share), p1 = min(n_part, p0 + share);
   const int col = blockIdx.y * 256 + lane * 8;
