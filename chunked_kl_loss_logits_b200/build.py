@@ -1,17 +1,22 @@
-"""Build libckl.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libckl.so (the C-ABI library) in-tree with nvcc for sm_100a, and the Python
+module that marshals the operators' calls to it (csrc/torch_ops.cpp, with g++ against
+the headers of the installed torch).
 
     python -m chunked_kl_loss_logits_b200.build [--verbose]
 
 Objects go to chunked_kl_loss_logits_b200/_build/, the library to
-chunked_kl_loss_logits_b200/lib/libckl.so. A source is recompiled only when it
-or a header is newer than its object.
+chunked_kl_loss_logits_b200/lib/libckl.so, the module beside it. A source is
+recompiled only when it or a header is newer than its object. The library needs no
+torch; without one the module is left out.
 """
 from __future__ import annotations
 
 import argparse
 import glob
+import importlib.util
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +24,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "lib", "libckl.so")
+OPS = os.path.join(PKG, "lib", "_ckl_ops.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -72,7 +78,30 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    build_ops()
     return LIB
+
+
+def build_ops():
+    """The Python module of the operators; its path, or None where torch is not installed."""
+    torch = importlib.util.find_spec("torch")  # found, not imported
+    if torch is None or not torch.origin:
+        return None
+    src, root = os.path.join(CSRC, "torch_ops.cpp"), os.path.dirname(torch.origin)
+    deps = [src, os.path.join(ROOT, "include", "ckl.h"), os.path.join(root, "version.py")]
+    if os.path.exists(OPS) and os.path.getmtime(OPS) >= max(map(os.path.getmtime, deps)):
+        return OPS
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           *["-I" + i for i in inc], src, "-o", OPS, "-L" + os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    return OPS
 
 
 if __name__ == "__main__":

@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 import threading
@@ -19,6 +21,7 @@ from torch.autograd.function import once_differentiable
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # The in-tree build; CKL_LIBRARY names another build of the same library.
 LIB_PATH = os.environ.get("CKL_LIBRARY") or os.path.join(_PKG, "lib", "libckl.so")
+OPS_PATH = os.path.join(_PKG, "lib", "_ckl_ops.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "ckl.h")
 
 F32, BF16 = 0, 1
@@ -221,9 +224,37 @@ def torch_vocab_group(V_total: int, group=None) -> VocabGroup:
 
 
 ACT8_FORMATS = {"int8": 0, "e4m3": 1}
+_ACT8_NAMES = ("int8", "e4m3")
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)  # the current stream's handle
+
+def _act8_format(fmt, what="fmt") -> int:
+    f = ACT8_FORMATS.get(fmt)
+    if f is None:
+        raise ValueError(f"{what} must be one of {sorted(ACT8_FORMATS)}")
+    return f
+
+_ops_module = None
+
+
+def _ops():
+    """The module that marshals the operators' calls, bound to the loaded library (raises if it
+    was not built)."""
+    global _ops_module
+    if _ops_module is None:
+        if not os.path.exists(OPS_PATH):
+            raise RuntimeError(f"{OPS_PATH} is missing: build it with "
+                               "`python -m chunked_kl_loss_logits_b200.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_ckl_ops", OPS_PATH)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_ckl_ops", loader))
+        loader.exec_module(m)
+        L = lib()
+        m.bind(CKLError, tuple(
+            ctypes.cast(getattr(L, "ckl_" + f), ctypes.c_void_p).value
+            for f in ("embed", "embed_grad_workspace_bytes", "embed_grad", "act8_pack",
+                      "act8_unpack", "act8_weight_grad_workspace_bytes", "act8_weight_grad", "norm",
+                      "norm_bwd_workspace_bytes", "norm_bwd")))
+        _ops_module = m
+    return _ops_module
 
 
 class Act8:
@@ -232,8 +263,7 @@ class Act8:
     an infinity or a NaN) and, from a norm, the rows' factors rstd (T, float32)."""
 
     def __init__(self, q, scale, fmt: str = "int8", rstd=None):
-        if fmt not in ACT8_FORMATS:
-            raise ValueError(f"fmt must be one of {sorted(ACT8_FORMATS)}")
+        _act8_format(fmt)
         if q.dtype != torch.uint8 or scale.dtype != torch.uint8:
             raise TypeError("q and scale must be uint8")
         if q.dim() != 2 or q.shape[1] == 0 or \
@@ -244,31 +274,28 @@ class Act8:
         for t in (q, scale) + ((rstd,) if rstd is not None else ()):
             if not t.is_contiguous() or t.device != q.device:
                 raise ValueError("q, scale and rstd must be contiguous tensors on one device")
-        self._parts, self.fmt, self.shape, self._index = (q, scale, rstd), fmt, tuple(q.shape), \
-            q.get_device()
-        self._ptrs = (q.data_ptr(), scale.data_ptr(), None if rstd is None else rstd.data_ptr())
+        self._parts, self._buf = (q, scale, rstd), None
+        self._desc = (q.data_ptr(), scale.data_ptr(), 0 if rstd is None else rstd.data_ptr(),
+                      *q.shape, ACT8_FORMATS[fmt], q.get_device(), rstd is not None)
+
+    __slots__ = ("_parts", "_buf", "_desc")
 
     @classmethod
-    def _in(cls, buf, T, cols, fmt, rstd: bool) -> "Act8":
-        """The checkpoint whose parts lie one after the other in `buf` (of _bytes() bytes): rstd,
-        then q from a multiple of 16 on, then scale."""
+    def _of(cls, buf, desc) -> "Act8":
+        """The checkpoint that the library's calls wrote to `buf`, as they describe it: rstd, then q
+        from a multiple of 16 on, then scale; desc = (addresses of q, scale and rstd, T, cols,
+        format, device index, has rstd)."""
         self = cls.__new__(cls)
-        at, p = (4 * T + 15) // 16 * 16 if rstd else 0, buf.data_ptr()
-        self._parts, self._buf, self._at = None, buf, at
-        self.fmt, self.shape, self._index = fmt, (T, cols), buf.get_device()
-        self._ptrs = (p + at, p + at + T * cols, p if rstd else None)
+        self._parts, self._buf, self._desc = None, buf, desc
         return self
-
-    @staticmethod
-    def _bytes(T, cols, rstd: bool) -> int:
-        return ((4 * T + 15) // 16 * 16 if rstd else 0) + T * (cols + (cols + 31) // 32)
 
     def _views(self):
         if self._parts is None:
-            (T, cols), at, b = self.shape, self._at, self._buf
-            n = T * cols
-            self._parts = (b[at:at + n].view(T, cols), b[at + n:].view(T, (cols + 31) // 32),
-                           b[:4 * T].view(torch.float32) if self._ptrs[2] is not None else None)
+            q, e, r, T, cols, _, _, has_rstd = self._desc
+            b, base = self._buf, self._buf.data_ptr()
+            self._parts = (b[q - base:q - base + T * cols].view(T, cols),
+                           b[e - base:].view(T, (cols + 31) // 32),
+                           b[:4 * T].view(torch.float32) if has_rstd else None)
         return self._parts
 
     @property
@@ -284,9 +311,17 @@ class Act8:
         return self._views()[2]
 
     @property
+    def fmt(self) -> str:
+        return _ACT8_NAMES[self._desc[5]]
+
+    @property
+    def shape(self) -> tuple:
+        return self._desc[3:5]
+
+    @property
     def nbytes(self) -> int:
         T, cols = self.shape
-        return T * (cols + (cols + 31) // 32 + (4 if self._ptrs[2] is not None else 0))
+        return T * (cols + (cols + 31) // 32 + (4 if self._desc[7] else 0))
 
 
 class ChunkedKL:
@@ -304,12 +339,14 @@ class ChunkedKL:
         _check(lib().ckl_create(ctypes.byref(h), dev.index or 0,
                                 F32 if dtype == torch.float32 else BF16, V, d, K, max_chunk),
                "ckl_create")
-        self._h, self._lib, self._index, self._ws_bytes = h, lib(), dev.index or 0, {}
+        self._h, self._index, self._ops = h, dev.index or 0, _ops()
+        self._ctx = (h.value, V, d, dtype == torch.bfloat16, self._index)
 
     def close(self):
         if getattr(self, "_h", None):
             lib().ckl_destroy(self._h)
             self._h = None
+            self._ctx = (0,) + self._ctx[1:]  # calls on a closed handle are refused
 
     def __del__(self):
         try:
@@ -538,75 +575,37 @@ class ChunkedKL:
         return idx, logit
 
     # ------------------------------------------------------------------ operators around the loss
-    # These calls are short, so their checks cost what the kernels of a small step do: plain
-    # comparisons, integers for pointers, sizes asked for once.
-    def _rows(self, name, t, *shape):
-        """t is a dense tensor of the handle's dtype on its device, of this shape if given."""
-        if t.dtype is not self.dtype:
-            raise TypeError(f"{name} must be {self.dtype}")
-        if (shape and t.shape != shape) or not t.is_contiguous() or t.get_device() != self._index:
-            self._dense(name, t, *shape)
-
-    def _f32(self, name, t, *shape):
-        if t.dtype is not torch.float32 or t.shape != shape:
-            raise TypeError(f"{name} must be a float32 tensor of shape {shape}")
-        self._dense(name, t)
-
-    def _dense(self, name, t, *shape):
-        if shape and t.shape != shape:
-            raise ValueError(f"{name} must have the shape {shape}")
-        if not t.is_contiguous() or t.get_device() != self._index:
-            raise ValueError(f"{name} must be a contiguous tensor on the handle's device")
-
+    # Checks, allocations and the call are made in csrc/torch_ops.cpp. Tensors must be dense, of the
+    # handle's dtype and on its device; `stream` (by default the current one) is where the call
+    # runs and what it allocates is allocated.
     @contextlib.contextmanager
     def _on(self, stream):
-        """The call, and what it allocates, on another stream of the handle's device."""
         if stream.device.index != self._index:
             raise ValueError("stream must be one of the handle's device")
         with torch.cuda.stream(stream):
             yield
 
-    def _ids(self, ids, mask):
-        if ids.dtype is not torch.int32:
-            raise TypeError("ids must be int32")
-        self._dense("ids", ids)
-        if mask is None:
-            return None
-        if mask.dtype is not torch.uint8 or mask.numel() != ids.numel():
-            raise TypeError("mask must be a uint8 tensor with an entry for each id")
-        self._dense("mask", mask)
-        return mask.data_ptr()
-
-    def _ckpt(self, ckpt: Act8, rows=None, cols=None) -> int:
-        T, c = ckpt.shape
-        if (rows is not None and T != rows) or (cols is not None and c != cols):
-            raise ValueError(f"the checkpoint must be {rows if rows is not None else T} x "
-                             f"{cols if cols is not None else c}")
-        if ckpt._index != self._index:
-            raise ValueError("the checkpoint must be on the handle's device")
-        return ACT8_FORMATS[ckpt.fmt]
-
-    def _new_act8(self, T, cols, fmt, rstd) -> Act8:
-        buf = torch.empty(Act8._bytes(T, cols, rstd), dtype=torch.uint8, device=self.device)
-        return Act8._in(buf, T, cols, fmt, rstd)
-
     def _workspace(self, query, *sizes) -> torch.Tensor:
         """A workspace of the size that the library's `query` gives for these sizes."""
-        key = (query, *sizes)
-        n = self._ws_bytes.get(key)
-        if n is None:
-            out = _SZ()
-            _check(getattr(lib(), query)(self._h, *sizes, ctypes.byref(out)), query)
-            if len(self._ws_bytes) >= 256:
-                self._ws_bytes.clear()
-            n = self._ws_bytes[key] = out.value
-        return torch.empty(n, dtype=torch.uint8, device=self.device)
+        n = _SZ()
+        _check(getattr(lib(), query)(self._h, *sizes, ctypes.byref(n)), query)
+        return torch.empty(n.value, dtype=torch.uint8, device=self.device)
 
-    def _given(self, workspace):
-        if workspace.dtype is not torch.uint8:
-            raise TypeError("workspace must be uint8")
-        self._dense("workspace", workspace)
-        return workspace
+    def embed_grad_workspace(self, T: int) -> torch.Tensor:
+        return self._workspace("ckl_embed_grad_workspace_bytes", T)
+
+    def norm_bwd_workspace(self, T: int) -> torch.Tensor:
+        return self._workspace("ckl_norm_bwd_workspace_bytes", T)
+
+    def act8_weight_grad_workspace(self, T: int, n: int, cols: int) -> torch.Tensor:
+        return self._workspace("ckl_act8_weight_grad_workspace_bytes", T, n, cols)
+
+    def act8_empty(self, T: int, cols: int, fmt: str = "int8", rstd: bool = False) -> Act8:
+        """Buffers for a checkpoint of T x cols (for a norm's with rstd=True), to write to later."""
+        at, nb = (4 * T + 15) // 16 * 16 if rstd else 0, (cols + 31) // 32
+        buf = torch.empty(at + T * (cols + nb), dtype=torch.uint8, device=self.device)
+        return Act8(buf[at:at + T * cols].view(T, cols), buf[at + T * cols:].view(T, nb), fmt,
+                    buf[:4 * T].view(torch.float32) if rstd else None)
 
     def embed(self, ids, W, mask=None, scale: float = 1.0, V_total: int | None = None, v0: int = 0,
               out=None, sync: bool = True, stream=None):
@@ -615,17 +614,7 @@ class ChunkedKL:
         if stream is not None:
             with self._on(stream):
                 return self.embed(ids, W, mask, scale, V_total, v0, out, sync)
-        m = self._ids(ids, mask)
-        self._rows("W", W, self.V, self.d)
-        if out is None:
-            out = torch.empty(*ids.shape, self.d, dtype=self.dtype, device=self.device)
-        else:
-            self._rows("out", out, *ids.shape, self.d)
-        code = self._lib.ckl_embed(self._h, ids.data_ptr(), m, W.data_ptr(), ids.numel(),
-                                   self.V if V_total is None else V_total, v0, scale,
-                                   out.data_ptr(), _raw_stream(self._index), sync)
-        _check(code, "ckl_embed")
-        return out
+        return self._ops.embed(self._ctx, ids, W, mask, scale, V_total, v0, out, sync)
 
     def embed_vocab_parallel(self, group: VocabGroup, ids, W_shard, mask=None, scale: float = 1.0,
                              sync: bool = True, stream=None):
@@ -634,15 +623,23 @@ class ChunkedKL:
         if stream is not None:
             with self._on(stream):
                 return self.embed_vocab_parallel(group, ids, W_shard, mask, scale, sync)
-        m = self._ids(ids, mask)
-        self._rows("W_shard", W_shard, self.V, self.d)
+        if ids.dtype != torch.int32 or W_shard.dtype != self.dtype:
+            raise TypeError(f"ids must be int32 and W_shard {self.dtype}")
+        if mask is not None and (mask.dtype != torch.uint8 or mask.numel() != ids.numel()):
+            raise TypeError("mask must be a uint8 tensor with an entry for each id")
+        if tuple(W_shard.shape) != (self.V, self.d):
+            raise ValueError("W_shard must be V x d")
+        for t in (ids, W_shard) + ((mask,) if mask is not None else ()):
+            if not t.is_contiguous() or t.device != self.device:
+                raise ValueError("inputs must be contiguous tensors on the handle's device")
         out = torch.empty(*ids.shape, self.d, dtype=self.dtype, device=self.device)
         ws = self._workspace("ckl_embed_vp_workspace_bytes", ids.numel())
         g, keep = group._c(self.device)
         group.error = None
-        code = self._lib.ckl_embed_vocab_parallel(
-            self._h, ctypes.byref(g), ids.data_ptr(), m, W_shard.data_ptr(), ids.numel(), scale,
-            out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(self._index), sync)
+        code = lib().ckl_embed_vocab_parallel(
+            self._h, ctypes.byref(g), _ptr(ids), _ptr(mask), _ptr(W_shard), ids.numel(), scale,
+            _ptr(out), _ptr(ws), ws.numel(),
+            ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream), int(sync))
         del keep
         if code == 9 and group.error is not None:
             raise CKLError(code, "ckl_embed_vocab_parallel") from group.error
@@ -656,25 +653,10 @@ class ChunkedKL:
         head's dW from fwd_bwd) and overwritten otherwise, or a new one."""
         if stream is not None:
             with self._on(stream):
-                return self.embed_grad(ids, dX, mask, scale, V_total, v0,
-                                       dW, accumulate, workspace, sync)
-        m = self._ids(ids, mask)
-        self._rows("dX", dX, *ids.shape, self.d)
-        if dW is None:
-            if accumulate:
-                raise ValueError("accumulate needs dW")
-            dW = torch.empty(self.V, self.d, dtype=torch.float32, device=self.device)
-        else:
-            self._f32("dW", dW, self.V, self.d)
-        T = ids.numel()
-        ws = self._workspace("ckl_embed_grad_workspace_bytes", T) if workspace is None else \
-            self._given(workspace)
-        code = self._lib.ckl_embed_grad(
-            self._h, ids.data_ptr(), m, dX.data_ptr(), T, self.V if V_total is None else V_total,
-            v0, scale, accumulate, dW.data_ptr(), ws.data_ptr(), ws.numel(),
-            _raw_stream(self._index), sync)
-        _check(code, "ckl_embed_grad")
-        return dW
+                return self.embed_grad(ids, dX, mask, scale, V_total, v0, dW, accumulate,
+                                       workspace, sync)
+        return self._ops.embed_grad(self._ctx, ids, dX, mask, scale, V_total, v0, dW, accumulate,
+                                    workspace, sync)
 
     def act8_pack(self, x, fmt: str = "int8", out: Act8 | None = None, stream=None) -> Act8:
         """The 8-bit checkpoint of x (T x cols, any cols that is a multiple of 8). With `out`, its
@@ -682,35 +664,17 @@ class ChunkedKL:
         if stream is not None:
             with self._on(stream):
                 return self.act8_pack(x, fmt, out)
-        self._rows("x", x)
-        if x.dim() != 2:
-            raise ValueError("x must be T x cols")
-        T, cols = x.shape
-        if out is None:
-            if fmt not in ACT8_FORMATS:
-                raise ValueError(f"fmt must be one of {sorted(ACT8_FORMATS)}")
-            out = self._new_act8(T, cols, fmt, False)
-        f = self._ckpt(out, T, cols)
-        code = self._lib.ckl_act8_pack(self._h, x.data_ptr(), T, cols, f, *out._ptrs[:2],
-                                       _raw_stream(self._index))
-        _check(code, "ckl_act8_pack")
-        return out
+        if out is not None:
+            self._ops.act8_pack(self._ctx, x, 0, out._desc)
+            return out
+        return Act8._of(*self._ops.act8_pack(self._ctx, x, _act8_format(fmt), None))
 
     def act8_unpack(self, ckpt: Act8, out=None, stream=None):
         """The values of a checkpoint (T x cols, the handle's dtype)."""
         if stream is not None:
             with self._on(stream):
                 return self.act8_unpack(ckpt, out)
-        f = self._ckpt(ckpt)
-        T, cols = ckpt.shape
-        if out is None:
-            out = torch.empty(T, cols, dtype=self.dtype, device=self.device)
-        else:
-            self._rows("out", out, T, cols)
-        code = self._lib.ckl_act8_unpack(self._h, *ckpt._ptrs[:2], T, cols, f, out.data_ptr(),
-                                         _raw_stream(self._index))
-        _check(code, "ckl_act8_unpack")
-        return out
+        return self._ops.act8_unpack(self._ctx, ckpt._desc, out)
 
     def act8_weight_grad(self, dY, ckpt: Act8, dW=None, accumulate: bool = False, workspace=None,
                          sync: bool = True, stream=None):
@@ -719,25 +683,7 @@ class ChunkedKL:
         if stream is not None:
             with self._on(stream):
                 return self.act8_weight_grad(dY, ckpt, dW, accumulate, workspace, sync)
-        f = self._ckpt(ckpt)
-        T, cols = ckpt.shape
-        self._rows("dY", dY)
-        if dY.dim() != 2 or dY.shape[0] != T:
-            raise ValueError("dY must be T x n, a row for each row of the checkpoint")
-        n = dY.shape[1]
-        if dW is None:
-            if accumulate:
-                raise ValueError("accumulate needs dW")
-            dW = torch.empty(n, cols, dtype=torch.float32, device=self.device)
-        else:
-            self._f32("dW", dW, n, cols)
-        ws = self._workspace("ckl_act8_weight_grad_workspace_bytes", T, n, cols) \
-            if workspace is None else self._given(workspace)
-        code = self._lib.ckl_act8_weight_grad(
-            self._h, dY.data_ptr(), T, n, *ckpt._ptrs[:2], cols, f, accumulate,
-            dW.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(self._index), sync)
-        _check(code, "ckl_act8_weight_grad")
-        return dW
+        return self._ops.act8_weight_grad(self._ctx, dY, ckpt._desc, dW, accumulate, workspace, sync)
 
     def norm(self, x, gain, residual=None, eps: float = 1e-5, checkpoint: str | None = "int8",
              out=None, stream=None):
@@ -748,36 +694,17 @@ class ChunkedKL:
         if stream is not None:
             with self._on(stream):
                 return self.norm(x, gain, residual, eps, checkpoint, out)
-        T, d = x.shape[0], self.d
-        self._rows("x", x, T, d)
-        self._rows("gain", gain, d)
-        if residual is not None:
-            self._rows("residual", residual, T, d)
-        if checkpoint is not None and checkpoint not in ACT8_FORMATS:
-            raise ValueError(f"checkpoint must be None or one of {sorted(ACT8_FORMATS)}")
+        fmt = -1 if checkpoint is None else _act8_format(checkpoint, "checkpoint")
         if out is None:
-            y = torch.empty_like(x)
-            s = x if residual is None else torch.empty_like(x)
-            ckpt = None if checkpoint is None else self._new_act8(T, d, checkpoint, True)
-        else:
-            y, s, ckpt = out
-            self._rows("out[0]", y, T, d)
-            if residual is None:
-                s = x
-            else:
-                self._rows("out[1]", s, T, d)
-            if (ckpt is None) != (checkpoint is None):
-                raise ValueError("out[2] must be an Act8 where a checkpoint is asked for")
-            if ckpt is not None and (ckpt.fmt != checkpoint or ckpt._ptrs[2] is None):
-                raise ValueError("out[2] must be a checkpoint with rstd in that format")
-        f, kept = 0, (None, None, None)
-        if ckpt is not None:
-            f, kept = self._ckpt(ckpt, T, d), ckpt._ptrs
-        code = self._lib.ckl_norm(
-            self._h, x.data_ptr(), None if residual is None else residual.data_ptr(),
-            gain.data_ptr(), T, eps, f, None if residual is None else s.data_ptr(), y.data_ptr(),
-            *kept, _raw_stream(self._index))
-        _check(code, "ckl_norm")
+            y, s, buf, desc = self._ops.norm(self._ctx, x, gain, residual, eps, fmt, None, None, None)
+            return y, s, None if desc is None else Act8._of(buf, desc)
+        y, s, ckpt = out
+        if (ckpt is None) != (checkpoint is None):
+            raise ValueError("out[2] must be an Act8 where a checkpoint is asked for")
+        if ckpt is not None and (ckpt._desc[5] != fmt or not ckpt._desc[7]):
+            raise ValueError("out[2] must be a checkpoint with rstd in that format")
+        y, s, _, _ = self._ops.norm(self._ctx, x, gain, residual, eps, fmt, y, s,
+                                    None if ckpt is None else ckpt._desc)
         return y, s, ckpt
 
     def norm_bwd(self, dY, ckpt: Act8, gain, d_residual=None, dX=None, dgain=None,
@@ -788,32 +715,8 @@ class ChunkedKL:
         if stream is not None:
             with self._on(stream):
                 return self.norm_bwd(dY, ckpt, gain, d_residual, dX, dgain, accumulate, workspace)
-        T, d = ckpt.shape[0], self.d
-        f = self._ckpt(ckpt, None, d)
-        if ckpt._ptrs[2] is None:
-            raise ValueError("the checkpoint has no rstd: it is not one of a norm")
-        self._rows("dY", dY, T, d)
-        self._rows("gain", gain, d)
-        if d_residual is not None:
-            self._rows("d_residual", d_residual, T, d)
-        if dX is None:
-            dX = torch.empty_like(dY)
-        else:
-            self._rows("dX", dX, T, d)
-        if dgain is None:
-            if accumulate:
-                raise ValueError("accumulate needs dgain")
-            dgain = torch.empty(d, dtype=torch.float32, device=self.device)
-        else:
-            self._f32("dgain", dgain, d)
-        ws = self._workspace("ckl_norm_bwd_workspace_bytes", T) if workspace is None else \
-            self._given(workspace)
-        code = self._lib.ckl_norm_bwd(
-            self._h, dY.data_ptr(), *ckpt._ptrs, gain.data_ptr(),
-            None if d_residual is None else d_residual.data_ptr(), T, f, accumulate, dX.data_ptr(),
-            dgain.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(self._index))
-        _check(code, "ckl_norm_bwd")
-        return dX, dgain
+        return self._ops.norm_bwd(self._ctx, dY, ckpt._desc, gain, d_residual, dX, dgain, accumulate,
+                                  workspace)
 
     def fwd_bwd_from_host(self, H_host, idx_host, logit_host, mask_host, staging, W, chunk,
                           out, workspace, stream=None) -> float:
@@ -978,8 +881,8 @@ class _RmsNormFn(torch.autograd.Function):
         res = None if residual is None else residual.detach().view(-1, handle.d)
         y, s, ckpt = handle.norm(flat, gain.detach(), res, eps, fmt)
         ctx.save_for_backward(ckpt._buf, gain)
-        ctx.rows = flat.shape[0]
-        ctx.fmt, ctx.handle, ctx.has_residual = fmt, handle, residual is not None
+        ctx.desc, ctx.handle, ctx.has_residual = ckpt._desc, handle, residual is not None
+        ctx.base = ckpt._buf.data_ptr()
         ctx.set_materialize_grads(False)
         return y.view(x.shape) if residual is None else (y.view(x.shape), s.view(x.shape))
 
@@ -991,7 +894,9 @@ class _RmsNormFn(torch.autograd.Function):
             return d_sum, None, d_sum if ctx.has_residual else None, None, None, None
         h = ctx.handle
         flat = [None if g is None else g.contiguous().view(-1, h.d) for g in (dY, d_sum)]
-        ckpt = Act8._in(buf, ctx.rows, h.d, ctx.fmt, True)
+        # what was saved may have been away (saved-tensor hooks) and be back at another address
+        to = buf.data_ptr() - ctx.base
+        ckpt = Act8._of(buf, tuple(p + to for p in ctx.desc[:3]) + ctx.desc[3:])
         dX, dgain = h.norm_bwd(flat[0], ckpt, gain.detach(), flat[1])
         dX = dX.view(dY.shape)
         return dX, dgain.to(gain.dtype), dX if ctx.has_residual else None, None, None, None

@@ -218,7 +218,7 @@ def test_calls_captured_in_a_graph_and_on_a_stream():
     ids, mask, W, dX = case(3000, 264, 900, "bf16", masked=True, hot=0.2)
     h = ckl.operator_handle(W, V=900)
     out, dW = torch.empty_like(dX), torch.empty(900, 264, device="cuda")
-    ws = h._workspace("ckl_embed_grad_workspace_bytes", 3000)
+    ws = h.embed_grad_workspace(3000)
     call = lambda: (h.embed(ids, W, mask=mask, out=out, sync=False),
                     h.embed_grad(ids, dX, mask=mask, dW=dW, workspace=ws, sync=False))
     s = torch.cuda.Stream()

@@ -173,7 +173,7 @@ def test_norm_in_place_and_given_buffers():
     h = ckl.operator_handle(x)
     y, s, c = h.norm(x, gain, residual=r)
     x2, r2 = x.clone(), r.clone()
-    c2 = h._new_act8(T, d, "int8", True)
+    c2 = h.act8_empty(T, d, "int8", rstd=True)
     y2, s2, c3 = h.norm(x2, gain, residual=r2, out=(x2, r2, c2))  # y over x, s over r
     assert y2 is x2 and s2 is r2 and c3 is c2
     assert torch.equal(x2, y) and torch.equal(r2, s)
@@ -240,9 +240,9 @@ def test_calls_captured_in_a_graph():
     x, r, dY = rows(T, d, "bf16"), rows(T, d, "bf16", 1), rows(T, d, "bf16", 2)
     gain = torch.ones(d, device="cuda", dtype=torch.bfloat16)
     h = ckl.operator_handle(x)
-    out = (torch.empty_like(x), torch.empty_like(x), h._new_act8(T, d, "e4m3", True))
+    out = (torch.empty_like(x), torch.empty_like(x), h.act8_empty(T, d, "e4m3", rstd=True))
     dX, dg = torch.empty_like(x), torch.empty(d, device="cuda")
-    ws = h._workspace("ckl_norm_bwd_workspace_bytes", T)
+    ws = h.norm_bwd_workspace(T)
 
     def call():
         h.norm(x, gain, residual=r, checkpoint="e4m3", out=out)
@@ -306,6 +306,69 @@ def test_autograd_rms_norm(residual):
         x.grad = r.grad = gain.grad = None
         ckl.rms_norm(x, gain, residual=r)[1].sum().backward()  # only the sum is used
         assert torch.all(x.grad == 1) and torch.all(r.grad == 1) and gain.grad is None
+
+
+def test_saved_tensors_may_come_back_elsewhere():
+    """What autograd saved goes to the host and back to another address."""
+    x = rows(40, 136, "bf16")
+    gain = torch.ones(136, device="cuda", dtype=torch.bfloat16)
+    dY = rows(40, 136, "bf16", 2)
+    grads = []
+    for hooks in (False, True):
+        xp, gp = x.clone().requires_grad_(), gain.clone().requires_grad_()
+        if hooks:
+            with torch.autograd.graph.save_on_cpu():
+                y = ckl.rms_norm(xp, gp)
+        else:
+            y = ckl.rms_norm(xp, gp)
+        held = [torch.full((40 * 200,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        y.backward(dY)
+        del held
+        grads.append((xp.grad, gp.grad))
+    assert torch.equal(grads[0][0], grads[1][0]) and torch.equal(grads[0][1], grads[1][1])
+
+
+def test_calls_on_a_given_stream_and_from_threads():
+    import threading
+    x = rows(500, 520, "bf16")
+    gain = torch.ones(520, device="cuda", dtype=torch.bfloat16)
+    h = ckl.operator_handle(x)
+    y, _, c = h.norm(x, gain)
+    dX, dg = h.norm_bwd(x, c, gain)
+    p = h.act8_unpack(h.act8_pack(x, "e4m3"))
+    dW = h.act8_weight_grad(x, c)
+    torch.cuda.synchronize()
+    got, errs = {}, []
+
+    def work(k):
+        try:
+            h = ckl.operator_handle(x)  # each thread has its own
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                y, _, c = h.norm(x, gain, stream=s)
+                got[k] = (h, y, *h.norm_bwd(x, c, gain, stream=s),
+                          h.act8_unpack(h.act8_pack(x, "e4m3", stream=s), stream=s),
+                          h.act8_weight_grad(x, c, stream=s))
+            s.synchronize()
+        except Exception as e:
+            errs.append(e)
+
+    th = [threading.Thread(target=work, args=(k,)) for k in range(3)]
+    [t.start() for t in th]
+    [t.join(120) for t in th]
+    assert not errs, errs
+    assert len({id(g[0]) for g in got.values()} | {id(h)}) == 4
+    for g in got.values():
+        for a, b in zip(g[1:], (y, dX, dg, p, dW)):
+            assert torch.equal(a, b)
+
+
+def test_a_closed_handle_is_refused():
+    h = ckl.ChunkedKL(1, 64, 1, max_chunk=1)
+    h.close()
+    with pytest.raises(ckl.CKLError) as e:
+        h.act8_pack(rows(3, 64, "bf16"))
+    assert e.value.code == 1
 
 
 def test_refusals():

@@ -146,7 +146,7 @@ def test_long_checkpoints_pass_32_bit_offsets():
 def test_calls_captured_in_a_graph():
     h, dY, ckpt = inputs(3000, 136, 200, "bf16", "int8")
     dW = torch.empty(136, 200, device="cuda")
-    ws = h._workspace("ckl_act8_weight_grad_workspace_bytes", 3000, 136, 200)
+    ws = h.act8_weight_grad_workspace(3000, 136, 200)
     call = lambda: h.act8_weight_grad(dY, ckpt, dW=dW, workspace=ws, sync=False)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
