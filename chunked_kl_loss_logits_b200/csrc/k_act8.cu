@@ -97,9 +97,11 @@ __global__ void __launch_bounds__(256)
 template <typename T, int WPR, int VPT, bool BWD>
 struct NormCfg {
   static constexpr int kThreads = WPR * 32;
-  // blocks per SM: 24 warps' worth backward (the sums of dg are in registers; two blocks of 16
-  // warps still fit at one vector a lane: 79 us against 91 at d = 4096), 36 forward
-  static constexpr int kWant = (!BWD ? 36 : VPT == 1 && WPR == 16 ? 32 : 24) / WPR;
+  // Blocks per SM, in warps: 36 forward, 24 backward, whose sums of dg are in registers; 32 where a
+  // power of two fills them at one vector a lane (d = 4096: 79 us for 15 thousand rows against 91;
+  // rows of 6 or 12 warps lose 3% that way).
+  static constexpr bool kEven = VPT == 1 && (WPR & (WPR - 1)) == 0;
+  static constexpr int kWant = (!BWD ? 36 : kEven ? 32 : 24) / WPR;
   static constexpr int kPerSm = kWant < 1 ? 1 : kWant > 16 ? 16 : kWant;
   static constexpr size_t kStage = (size_t)kThreads * VPT * (2 * sizeof(Raw8<T>) + (BWD ? 8 : 0));
   static constexpr size_t kRoom = 200 * 1024 / kPerSm;

@@ -50,6 +50,32 @@ def test_act8_refuses_inconsistent_parts():
         ckl.Act8(q, e, rstd=torch.ones(3, dtype=torch.float64))
 
 
+def test_the_module_refuses_before_it_calls(L):
+    """The checks of the operators' module, on tensors that are not on a GPU: types and shapes
+    first, then the device; a null handle would be refused by the library only after them."""
+    m = ckl._ops()
+    ctx = (0, 30, 16, True, 0)
+    ids, W, x = torch.zeros(4, dtype=torch.int32), torch.zeros(30, 16).bfloat16(), \
+        torch.zeros(4, 16).bfloat16()
+    ck = ckl.Act8(torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.uint8))
+    T, V = TypeError, ValueError
+    for err, call in (
+            (T, lambda: m.embed(ctx, ids)),
+            (T, lambda: m.embed(ctx, ids.long(), W, None, 1.0, None, 0, None, False)),
+            (T, lambda: m.embed(ctx, [1, 2], W, None, 1.0, None, 0, None, False)),
+            (V, lambda: m.embed(ctx, ids, W, None, 1.0, None, 0, None, False)),  # on the CPU
+            (T, lambda: m.embed_grad(ctx, ids.float(), x, None, 1.0, None, 0, None, 0, None, 0)),
+            (T, lambda: m.norm(ctx, x.float(), x[0], None, 1e-5, -1, None, None, None)),
+            (V, lambda: m.norm(ctx, x[:, :8], x[0], None, 1e-5, -1, None, None, None)),
+            (T, lambda: m.norm(ctx, None, x[0], None, 1e-5, -1, None, None, None)),
+            (V, lambda: m.norm(ctx, x, x[0], None, 1e-5, -1, None, None, None)),
+            (V, lambda: m.norm_bwd(ctx, x, ck._desc, x[0], None, None, None, 0, None)),
+            (V, lambda: m.act8_unpack(ctx, ck._desc, None)),
+            (V, lambda: m.act8_pack(ctx, x, 0, None))):
+        with pytest.raises(err):
+            call()
+
+
 def test_operator_handle_refuses_cpu_tensors():
     with pytest.raises(ValueError):
         ckl.operator_handle(torch.zeros(2, 8))
