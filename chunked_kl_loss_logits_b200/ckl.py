@@ -577,7 +577,7 @@ class ChunkedKL:
     # ------------------------------------------------------------------ operators around the loss
     # Checks, allocations and the call are made in csrc/torch_ops.cpp. Tensors must be dense, of the
     # handle's dtype and on its device; `stream` (by default the current one) is where the call
-    # runs and what it allocates is allocated.
+    # runs and what it allocates is allocated. A call captured in a CUDA graph takes sync=False.
     @contextlib.contextmanager
     def _on(self, stream):
         if stream.device.index != self._index:
@@ -868,7 +868,9 @@ def embedding(ids, W, mask=None, scale: float = 1.0, handle: ChunkedKL | None = 
     gradient is formed in fp32 by sorted tokens and does not change from run to run.
 
     check=True: backward() waits and raises CKLError if an id was outside [0, V); check=False:
-    nothing waits and the status stays in the handle (operator_handle(W, W.shape[0]))."""
+    nothing waits and the status stays in the handle (operator_handle(W, W.shape[0])), as a step
+    captured in a CUDA graph needs. Before that capture, as with any operator: run the step once on
+    a side stream, and let go of whatever still holds an eager graph of the same leaves."""
     if handle is None:
         handle = operator_handle(W, W.shape[0])
     return _EmbeddingFn.apply(W, ids, mask, scale, handle, check)

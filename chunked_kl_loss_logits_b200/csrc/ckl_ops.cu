@@ -20,6 +20,20 @@ ckl_status cuda_status(cudaError_t err) {
   return CKL_ERR_CUDA;
 }
 
+// Set the handle's device, and see that a call that is to wait does not run on a stream whose work
+// is being captured: to wait would spoil the capture, so nothing is enqueued.
+ckl_status enter(DeviceGuard& guard, cudaStream_t s, int wait) {
+  if (!guard.ok) return CKL_ERR_CUDA;
+  cudaGetLastError();
+  if (!wait) return CKL_OK;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  const cudaError_t err = cudaStreamIsCapturing(s, &capture);
+  if (err == cudaSuccess && capture == cudaStreamCaptureStatusNone) return CKL_OK;
+  cudaGetLastError();
+  return err == cudaSuccess || err == cudaErrorStreamCaptureImplicit ? CKL_ERR_INVALID_ARG
+                                                                     : cuda_status(err);
+}
+
 size_t elem(const ckl_ctx* h) { return h->dtype == CKL_BF16 ? 2 : 4; }
 
 // ------------------------------------------------------------------ embedding
@@ -128,9 +142,8 @@ ckl_status ckl_act8_weight_grad(ckl_handle h, const void* dY, int64_t T, int64_t
   if (P.total && (!workspace || !aligned(workspace, 256) || workspace_bytes < P.total))
     return CKL_ERR_WORKSPACE;
   DeviceGuard guard(h->device);
-  if (!guard.ok) return CKL_ERR_CUDA;
-  cudaGetLastError();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = enter(guard, s, wait)) != CKL_OK) return st;
   cudaError_t err = cudaSuccess;
   auto chk = [&](cudaError_t e) { if (e != cudaSuccess && err == cudaSuccess) err = e; };
   if (T == 0) {
@@ -191,9 +204,8 @@ ckl_status ckl_embed(ckl_handle h, const int32_t* ids, const uint8_t* mask, cons
   if (!W || (T > 0 && !out)) return CKL_ERR_INVALID_ARG;
   if (!aligned(W, 16) || (out && !aligned(out, 16))) return CKL_ERR_ALIGNMENT;
   DeviceGuard guard(h->device);
-  if (!guard.ok) return CKL_ERR_CUDA;
-  cudaGetLastError();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = enter(guard, s, wait)) != CKL_OK) return st;
   if (T > 0) {
     Launcher L{h, s};
     st = cuda_status(L(KID_EMBED, 0, (double)T * h->d * 2 * elem(h), [&] {
@@ -226,9 +238,8 @@ ckl_status ckl_embed_vocab_parallel(ckl_handle h, const ckl_vocab_group* g, cons
   if (T > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
     return CKL_ERR_WORKSPACE;
   DeviceGuard guard(h->device);
-  if (!guard.ok) return CKL_ERR_CUDA;
-  cudaGetLastError();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = enter(guard, s, wait)) != CKL_OK) return st;
   if (T > 0) {
     Launcher L{h, s};
     float* buf = static_cast<float*>(workspace);
@@ -268,9 +279,8 @@ ckl_status ckl_embed_grad(ckl_handle h, const int32_t* ids, const uint8_t* mask,
   if (T > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < P.total))
     return CKL_ERR_WORKSPACE;
   DeviceGuard guard(h->device);
-  if (!guard.ok) return CKL_ERR_CUDA;
-  cudaGetLastError();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = enter(guard, s, wait)) != CKL_OK) return st;
   cudaError_t err = cudaSuccess;
   auto chk = [&](cudaError_t e) { if (e != cudaSuccess && err == cudaSuccess) err = e; };
   const int d = (int)h->d, V = (int)h->V;
@@ -308,9 +318,8 @@ ckl_status ckl_act8_pack(ckl_handle h, const void* X, int64_t T, int64_t cols, c
   if (X && !aligned(X, 16)) return CKL_ERR_ALIGNMENT;
   if (T == 0) return CKL_OK;
   DeviceGuard guard(h->device);
-  if (!guard.ok) return CKL_ERR_CUDA;
-  cudaGetLastError();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = enter(guard, s, 0)) != CKL_OK) return st;
   Launcher L{h, s};
   return cuda_status(L(KID_ACT8_PACK, 0, (double)T * cols * (elem(h) + 33.0 / 32), [&] {
     launch_act8_pack(h->dtype == CKL_BF16, X, T, (int)cols, fmt, static_cast<uint8_t*>(q), scale, s);
@@ -325,9 +334,8 @@ ckl_status ckl_act8_unpack(ckl_handle h, const void* q, const uint8_t* scale, in
   if (out && !aligned(out, 16)) return CKL_ERR_ALIGNMENT;
   if (T == 0) return CKL_OK;
   DeviceGuard guard(h->device);
-  if (!guard.ok) return CKL_ERR_CUDA;
-  cudaGetLastError();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = enter(guard, s, 0)) != CKL_OK) return st;
   Launcher L{h, s};
   return cuda_status(L(KID_ACT8_UNPACK, 0, (double)T * cols * (elem(h) + 33.0 / 32), [&] {
     launch_act8_unpack(h->dtype == CKL_BF16, static_cast<const uint8_t*>(q), scale, T, (int)cols,
@@ -349,9 +357,8 @@ ckl_status ckl_norm(ckl_handle h, const void* X, const void* residual, const voi
   if (rstd && !aligned(rstd, 4)) return CKL_ERR_ALIGNMENT;
   if (T == 0) return CKL_OK;
   DeviceGuard guard(h->device);
-  if (!guard.ok) return CKL_ERR_CUDA;
-  cudaGetLastError();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (const ckl_status st = enter(guard, s, 0); st != CKL_OK) return st;
   NormArgs a{};
   a.x = X; a.res = residual; a.gain = gain; a.T = T; a.d = (int)h->d; a.eps = eps; a.fmt = fmt;
   a.sum = sum; a.y = Y; a.q = static_cast<uint8_t*>(q); a.e = scale; a.rstd = rstd;
@@ -385,9 +392,8 @@ ckl_status ckl_norm_bwd(ckl_handle h, const void* dY, const void* q, const uint8
   if (T > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)rows * d * 4))
     return CKL_ERR_WORKSPACE;
   DeviceGuard guard(h->device);
-  if (!guard.ok) return CKL_ERR_CUDA;
-  cudaGetLastError();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = enter(guard, s, 0)) != CKL_OK) return st;
   if (T == 0) return accumulate ? CKL_OK : cuda_status(cudaMemsetAsync(dgain, 0, (size_t)d * 4, s));
   NormArgs a{};
   a.x = dY; a.res = d_sum; a.gain = gain; a.T = T; a.d = d; a.fmt = fmt; a.y = dX;

@@ -282,8 +282,9 @@ ckl_status ckl_topk_cache_vocab_parallel(ckl_handle h, const ckl_vocab_group* gr
  * the backward pass in 8 bits. They take a handle for its device, dtype and hidden size d
  * (the embedding also for V, the rows of W held; K and max_chunk do not matter to them).
  * The conventions at the top hold. T <= 2^31 - 1. All results are deterministic: no sum's
- * order depends on timing. All calls can be captured in a CUDA graph once each has run
- * (wait = 0 where there is that argument). */
+ * order depends on timing. All calls can be captured in a CUDA graph once each has run, with
+ * wait = 0 where there is that argument: wait != 0 on a stream that is being captured is
+ * refused with CKL_ERR_INVALID_ARG, nothing is enqueued and the capture can go on. */
 
 /* out[t] = scale * W[ids[t] - v0], rounded once to the handle's dtype (T x d).
  * mask may be NULL; a token with mask 0 gets a row of zeros and its id is not looked at.

@@ -1,0 +1,82 @@
+"""The operators' calls and their backward passes captured in CUDA graphs."""
+import pytest
+import torch
+
+from chunked_kl_loss_logits_b200 import ckl
+
+pytestmark = pytest.mark.gpu
+T, V, D = 300, 500, 264
+
+
+def inputs():
+    g = torch.Generator().manual_seed(3)
+    ids = torch.randint(0, V, (T,), generator=g, dtype=torch.int32).cuda()
+    W = torch.randn(V, D, generator=g).to(torch.bfloat16).cuda()
+    gain = (1 + 0.1 * torch.randn(D, generator=g)).to(torch.bfloat16).cuda()
+    return ids, W, gain
+
+
+def test_a_call_that_would_wait_is_refused_in_a_capture_that_goes_on():
+    ids, W, gain = inputs()
+    h = ckl.operator_handle(W, V)
+    x = h.embed(ids, W)
+    dW = h.embed_grad(ids, x)
+    c = h.act8_pack(x)
+    dL = h.act8_weight_grad(x, c)
+    torch.cuda.synchronize()
+    before = h.launch_count()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for call in (lambda: h.embed(ids, W), lambda: h.embed_grad(ids, x),
+                     lambda: h.act8_weight_grad(x, c)):
+            with pytest.raises(ckl.CKLError) as e:
+                call()
+            assert e.value.code == 1
+        assert h.launch_count() == before
+        out = h.embed(ids, W, sync=False)
+        dW2 = h.embed_grad(ids, x, sync=False)
+        dL2 = h.act8_weight_grad(x, c, sync=False)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, x) and torch.equal(dW2, dW) and torch.equal(dL2, dL)
+    h.sync_status()
+
+
+def test_a_backward_pass_captured():
+    """embedding and rms_norm with their backward passes in one graph, replayed on other ids."""
+    ids, W, gain = inputs()
+    W.requires_grad_()
+    gain.requires_grad_()
+    weight = torch.randn(T, D, device="cuda").to(torch.bfloat16)
+
+    def step():
+        x = ckl.embedding(ids, W, scale=2.0, check=False)
+        y, s = ckl.rms_norm(x, gain, residual=x.detach() * 0.5)
+        ((y * weight).sum() + s.sum()).backward()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            W.grad = gain.grad = None
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    W.grad = gain.grad = None
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    static = W.grad, gain.grad
+    replayed = []
+    for seed in (1, 2):
+        ids.copy_(torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(seed),
+                                dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        replayed.append((ids.clone(), static[0].clone(), static[1].clone()))
+    ckl.operator_handle(W, V).sync_status()
+    for k, gW, gg in replayed:
+        ids.copy_(k)
+        W.grad = gain.grad = None
+        step()
+        assert torch.equal(W.grad, gW) and torch.equal(gain.grad, gg)
