@@ -286,6 +286,14 @@ ckl_status ckl_embed_grad(ckl_handle h, const int32_t* ids, const uint8_t* mask,
   const int d = (int)h->d, V = (int)h->V;
   if (T == 0) {
     if (!accumulate) chk(cudaMemsetAsync(dW, 0, (size_t)V * d * 4, s));
+  } else if (embed_grad_is_few(T)) {
+    Launcher L{h, s};
+    if (!accumulate)
+      chk(L(KID_EMBED_ZERO, 0, 4.0 * V * d, [&] { launch_embed_zero(dW, (int64_t)V * d, s); }));
+    chk(L(KID_EMBED_GRAD, 0, (double)T * d * elem(h), [&] {
+      chk(launch_embed_grad_few(ids_of(h, ids, mask, T, V_total, v0), h->dtype == CKL_BF16, dX, d,
+                                scale, accumulate != 0, dW, s));
+    }));
   } else {
     unsigned char* base = static_cast<unsigned char*>(workspace);
     uint64_t* a = reinterpret_cast<uint64_t*>(base + P.off_a);

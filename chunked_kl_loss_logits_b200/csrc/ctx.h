@@ -29,7 +29,7 @@ enum KernelId {
   KID_DH_F32, KID_TO_BF16, KID_VP_GATHER, KID_VP_REDUCE,
   KID_EMBED, KID_EMBED_SORT, KID_EMBED_GRAD, KID_EMBED_JOIN, KID_ACT8_PACK, KID_ACT8_UNPACK,
   KID_NORM_FWD, KID_NORM_BWD, KID_NORM_DGAIN, KID_WGRAD_PARTS, KID_WGRAD, KID_WGRAD_SUM,
-  KID_COUNT
+  KID_EMBED_ZERO, KID_COUNT
 };
 // bf16 backward: a profiled "dh_gemm" range also holds the next chunk's teacher
 // kernel, and a "dw_gemm" range the chunk's dH split reduction, both launched
@@ -43,7 +43,7 @@ inline const char* const kKernelNames[KID_COUNT] = {"mask_count", "teacher_topk"
                                        "embed_grad", "embed_join", "act8_pack", "act8_unpack",
                                        "norm_fwd", "norm_bwd", "norm_dgain", "weight_grad_parts",
                                        "act8_weight_grad",
-                                       "weight_grad_sum"};
+                                       "weight_grad_sum", "embed_zero"};
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -413,6 +413,79 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// Few tokens: no sort. The CTA of a token and 256 columns compares the token's row with every
+// other's, gives way where an earlier token has the same row, and otherwise adds up the row's
+// tokens in order of position, each of the eight warps a contiguous share of them, then the eight in
+// order. One launch instead of three, each of which waits for the one before.
+constexpr int kFew = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    embed_grad_few_kernel(const EmbedIds a, const T* __restrict__ dX, int nvec, float scale,
+                          bool accumulate, float* dW) {
+  __shared__ uint32_t has[8];  // bit j: token j has this row
+  __shared__ uint8_t list[kFew];
+  __shared__ float4 sums[8][32][2];
+  const int n = (int)a.T, i = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = threadIdx.x;
+  bool bad = false, ignore = false;
+  const int32_t row = row_of(a, a.ids[i], a.mask ? a.mask[i] : 1, bad);
+  const int32_t other = j < n ? row_of(a, a.ids[j], a.mask ? a.mask[j] : 1, ignore) : a.V;
+  if (bad && j == 0 && blockIdx.y == 0) atomicOr(a.status, (unsigned)ST_INDEX_RANGE);
+  if (row == a.V) return;
+  const uint32_t mine = __ballot_sync(0xffffffffu, other == row);
+  if (lane == 0) has[warp] = mine;
+  __syncthreads();
+  int before = 0, count = 0;  // tokens of this row: in the words before this warp's, in all
+  bool first = true;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const uint32_t m = has[w];
+    before += w < warp ? __popc(m) : 0;
+    count += __popc(m);
+    first &= w * 32 >= i || (m & (i >= w * 32 + 32 ? ~0u : (1u << (i - w * 32)) - 1u)) == 0;
+  }
+  if (!first) return;
+  if (other == row) list[before + __popc(mine & ((1u << lane) - 1u))] = (uint8_t)j;
+  __syncthreads();
+  const int vec = blockIdx.y * 32 + lane;
+  const int share = (count + 7) / 8, p0 = min(count, warp * share), p1 = min(count, p0 + share);
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (vec < nvec) {
+#pragma unroll 8
+    for (int p = p0; p < p1; ++p) {
+      float f[8];
+      to_f32(load8(dX + ((int64_t)list[p] * nvec + vec) * 8), f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] += f[k];
+    }
+  }
+  if (count > 1) {
+    const Raw8<float> r = from_f32<float>(acc);
+    sums[warp][lane][0] = r.a;
+    sums[warp][lane][1] = r.b;
+    __syncthreads();
+  }
+  if (warp != 0 || vec >= nvec) return;
+  for (int w = 1; w * share < count; ++w) {
+    const Raw8<float> o{sums[w][lane][0], sums[w][lane][1]};
+    float f[8];
+    to_f32(o, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] += f[k];
+  }
+  griddep_wait();  // the zeros are written
+  add_row8(dW + ((int64_t)row * nvec + vec) * 8, acc, scale, accumulate);
+}
+
+__global__ void __launch_bounds__(1024) embed_zero_kernel(float4* dst, int64_t n) {
+  griddep_launch_dependents();
+  const int64_t i0 = (int64_t)blockIdx.x * kFillBlock + threadIdx.x;
+#pragma unroll 8
+  for (int64_t i = i0; i < min(n, i0 - threadIdx.x + kFillBlock); i += 1024)
+    dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
 // Digits of the sort: bits of the largest key (V), in as few equal digits as fit the bins.
 void sort_digits(int32_t V, int& n_pass, int& bits) {
   int need = 1;
@@ -471,6 +544,26 @@ cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a, n_pass, bits, cluster, buf_a, buf_b,
                             reinterpret_cast<float4*>(fill), n_fill / 4);
+}
+
+bool embed_grad_is_few(int64_t T) { return T <= kFew; }
+
+cudaError_t launch_embed_grad_few(const EmbedIds& a, bool bf16, const void* dX, int d, float scale,
+                                  bool accumulate, float* dW, cudaStream_t s) {
+  const dim3 grid((unsigned)a.T, (unsigned)((d + 255) / 256));
+  auto launch = [&](auto kernel, auto* x) {
+    // it reads ids and dX before its wait: behind the zeros only, whose launch waited for those
+    if (!accumulate) return launch_behind(kernel, grid, 256, 0, s, a, x, d / 8, scale, accumulate, dW);
+    kernel<<<grid, 256, 0, s>>>(a, x, d / 8, scale, accumulate, dW);
+    return cudaSuccess;
+  };
+  return bf16 ? launch(embed_grad_few_kernel<uint16_t>, (const uint16_t*)dX)
+              : launch(embed_grad_few_kernel<float>, (const float*)dX);
+}
+
+void launch_embed_zero(float* dst, int64_t n, cudaStream_t s) {
+  embed_zero_kernel<<<(unsigned)((n / 4 + kFillBlock - 1) / kFillBlock), 1024, 0, s>>>(
+      reinterpret_cast<float4*>(dst), n / 4);
 }
 
 // Lanes of a group: as many as a row has vectors of eight columns, or the most of 32, 16 and 8 that

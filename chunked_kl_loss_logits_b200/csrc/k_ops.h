@@ -27,6 +27,12 @@ void launch_embed(const EmbedIds& a, bool bf16, const void* W, int d, float scal
 int embed_sort_result(int32_t V);
 cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_b, float* fill,
                               int64_t n_fill, cudaStream_t s);
+// dW[row] (+)= scale * sum of the row's dX where that needs no sort (few tokens, by embed_grad_is_few).
+// Where dW is overwritten it follows launch_embed_zero (launch_behind).
+bool embed_grad_is_few(int64_t T);
+cudaError_t launch_embed_grad_few(const EmbedIds& a, bool bf16, const void* dX, int d, float scale,
+                                  bool accumulate, float* dW, cudaStream_t s);
+void launch_embed_zero(float* dst, int64_t n, cudaStream_t s);  // n: a multiple of 8
 // How the gradient is shared out: groups of `lanes` threads walk `run` sorted tokens each,
 // 256 / lanes groups make a CTA's tile, `slabs` CTAs cover the columns.
 struct EmbedShape {

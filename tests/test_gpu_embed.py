@@ -306,3 +306,48 @@ def test_refusals():
     with pytest.raises(ckl.CKLError) as e:
         h.embed(ids, shifted)
     assert e.value.code == 7
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 31, 32, 33, 255, 256, 257])
+@pytest.mark.parametrize("hot", [0, 0.6, 1])
+def test_embed_grad_of_few_tokens(T, hot, dt):
+    """Both sides of where the sort begins: rows met once, a row met by most tokens, by all; a
+    last column block that is not full; overwritten, added to, and on a shard."""
+    d, V = 520, 90
+    ids, mask, W, dX = case(T, d, V, dt, masked=True, hot=hot)
+    dX[mask == 0] = float("inf")
+    ids[mask == 0] = -7
+    h = ckl.operator_handle(W, V=V)
+    base = torch.randn(V, d, device="cuda")
+    clean = torch.where((mask != 0)[:, None], dX, torch.zeros_like(dX))
+    look = torch.where(mask != 0, ids, torch.zeros_like(ids))
+    got = h.embed_grad(ids, dX, mask=mask, scale=1.7)
+    check_grad(got, look, clean, V, mask, float(np.float32(1.7)), None)
+    assert torch.equal(got, h.embed_grad(ids, dX, mask=mask, scale=1.7))
+    more = h.embed_grad(ids, dX, mask=mask, scale=1.7, dW=base.clone(), accumulate=True)
+    check_grad(more, look, clean, V, mask, float(np.float32(1.7)), base)
+    s = ckl.operator_handle(W, V=50)
+    part = s.embed_grad(ids, dX, mask=mask, scale=1.7, V_total=V, v0=30)
+    # (not the same bits as got[30:80]: how a sorted row's tokens are grouped depends on where it is)
+    check_grad(part, look, clean, 50, mask, float(np.float32(1.7)), v0=30)
+
+
+def test_embed_grad_of_few_tokens_behind_another_call():
+    """Its inputs written by the call before it, which lets what follows start early."""
+    T, d, V = 200, 2048, 300
+    ids, _, _, dX = case(T, d, V, "bf16")
+    x = torch.randn(T, d, device="cuda").to(torch.bfloat16)
+    gain = torch.ones(d, device="cuda", dtype=torch.bfloat16)
+    h, he = ckl.operator_handle(x), ckl.operator_handle(x, V=V)
+    _, _, c = h.norm(x, gain)
+    dW = torch.zeros(V, d, device="cuda")
+    for k in range(20):
+        dY = (dX * (k + 1)).contiguous()
+        ref = he.embed_grad(ids, h.norm_bwd(dY, c, gain)[0].clone())
+        out = torch.full_like(dY, float("nan"))
+        dW.zero_()
+        h.norm_bwd(dY, c, gain, dX=out)
+        he.embed_grad(ids, out, dW=dW, accumulate=True, sync=False)
+        torch.cuda.synchronize()
+        assert torch.equal(dW, ref)
