@@ -413,68 +413,95 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Few tokens: no sort. The CTA of a token and 256 columns compares the token's row with every
-// other's, gives way where an earlier token has the same row, and otherwise adds up the row's
-// tokens in order of position, each of the eight warps a contiguous share of them, then the eight in
-// order. One launch instead of three, each of which waits for the one before.
-constexpr int kFew = 256;
+// Few tokens: no sort. A token's CTA compares its row with every other token's. The row's c tokens
+// have c CTAs: the one of the m-th takes the m-th of every c slabs of 256 columns. Its warps
+// take a slab each where it has many, or share one slab's tokens: each a contiguous part of them in
+// order of position, and the parts are added up in order. One launch instead of three, each of
+// which waits for the one before.
+constexpr int kFew = 1024;
+constexpr int kFewWords = kFew / 32;
 
 template <typename T>
 __global__ void __launch_bounds__(256)
     embed_grad_few_kernel(const EmbedIds a, const T* __restrict__ dX, int nvec, float scale,
                           bool accumulate, float* dW) {
-  __shared__ uint32_t has[8];  // bit j: token j has this row
-  __shared__ uint8_t list[kFew];
+  static_assert(kFewWords == 32, "a word of the tokens' bits for each lane");
+  __shared__ uint32_t has[kFewWords];  // bit j: token j has this row
+  __shared__ uint16_t list[kFew];      // those tokens
   __shared__ float4 sums[8][32][2];
   const int n = (int)a.T, i = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int j = threadIdx.x;
   bool bad = false, ignore = false;
   const int32_t row = row_of(a, a.ids[i], a.mask ? a.mask[i] : 1, bad);
-  const int32_t other = j < n ? row_of(a, a.ids[j], a.mask ? a.mask[j] : 1, ignore) : a.V;
-  if (bad && j == 0 && blockIdx.y == 0) atomicOr(a.status, (unsigned)ST_INDEX_RANGE);
+  if (bad && threadIdx.x == 0) atomicOr(a.status, (unsigned)ST_INDEX_RANGE);
   if (row == a.V) return;
-  const uint32_t mine = __ballot_sync(0xffffffffu, other == row);
-  if (lane == 0) has[warp] = mine;
-  __syncthreads();
-  int before = 0, count = 0;  // tokens of this row: in the words before this warp's, in all
-  bool first = true;
+  uint32_t mine[kFewWords / 8];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const uint32_t m = has[w];
-    before += w < warp ? __popc(m) : 0;
-    count += __popc(m);
-    first &= w * 32 >= i || (m & (i >= w * 32 + 32 ? ~0u : (1u << (i - w * 32)) - 1u)) == 0;
+  for (int k = 0; k < kFewWords / 8; ++k) {
+    const int j = k * 256 + (int)threadIdx.x;
+    const bool same = j < n && row_of(a, a.ids[j], a.mask ? a.mask[j] : 1, ignore) == row;
+    mine[k] = __ballot_sync(0xffffffffu, same);
+    if (lane == 0) has[k * 8 + warp] = mine[k];
   }
-  if (!first) return;
-  if (other == row) list[before + __popc(mine & ((1u << lane) - 1u))] = (uint8_t)j;
   __syncthreads();
-  const int vec = blockIdx.y * 32 + lane;
-  const int share = (count + 7) / 8, p0 = min(count, warp * share), p1 = min(count, p0 + share);
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (vec < nvec) {
-#pragma unroll 8
-    for (int p = p0; p < p1; ++p) {
-      float f[8];
-      to_f32(load8(dX + ((int64_t)list[p] * nvec + vec) * 8), f);
+  const uint32_t word = has[lane];
+  const uint32_t below = lane < i / 32 ? ~0u : lane > i / 32 ? 0u : (1u << (i & 31)) - 1u;
+  const int m = (int)__reduce_add_sync(0xffffffffu, __popc(word & below));
+  int upto = __popc(word);  // tokens in the words up to this lane's
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += f[k];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  const int c = __shfl_sync(0xffffffffu, upto, 31), slabs = (nvec + 31) / 32;
+  if (m >= slabs) return;
+#pragma unroll
+  for (int k = 0; k < kFewWords / 8; ++k) {
+    const int before = __shfl_sync(0xffffffffu, upto - __popc(word), k * 8 + warp);
+    if (mine[k] >> lane & 1u)
+      list[before + __popc(mine[k] & ((1u << lane) - 1u))] = (uint16_t)(k * 256 + threadIdx.x);
+  }
+  __syncthreads();
+  const int ns = (slabs - m + c - 1) / c;  // slabs of this CTA
+  const int per = ns > 4 ? 1 : ns > 2 ? 2 : ns > 1 ? 4 : 8;  // warps for a slab
+  const int group = warp / per, sub = warp % per, share = (c + per - 1) / per;
+  const int p0 = min(c, sub * share), p1 = min(c, p0 + share);
+  bool wrote = false;
+  for (int q = group; q < ns; q += 8 / per) {  // (at most one where warps share a slab)
+    const int vec = (m + q * c) * 32 + lane;
+    const bool on = vec < nvec;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (on) {
+#pragma unroll 8
+      for (int p = p0; p < p1; ++p) {
+        float f[8];
+        to_f32(load8(dX + ((int64_t)list[p] * nvec + vec) * 8), f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += f[k];
+      }
+    }
+    if (per > 1 && c > 1) {
+      const Raw8<float> r = from_f32<float>(acc);
+      sums[warp][lane][0] = r.a;
+      sums[warp][lane][1] = r.b;
+    } else if (on && sub == 0) {
+      if (!wrote) griddep_wait();  // the zeros are written
+      wrote = true;
+      add_row8(dW + ((int64_t)row * nvec + vec) * 8, acc, scale, accumulate);
     }
   }
-  if (count > 1) {
-    const Raw8<float> r = from_f32<float>(acc);
-    sums[warp][lane][0] = r.a;
-    sums[warp][lane][1] = r.b;
-    __syncthreads();
-  }
-  if (warp != 0 || vec >= nvec) return;
-  for (int w = 1; w * share < count; ++w) {
-    const Raw8<float> o{sums[w][lane][0], sums[w][lane][1]};
+  if (per == 1 || c == 1) return;
+  __syncthreads();
+  const int vec = (m + group * c) * 32 + lane;
+  if (sub != 0 || group >= ns || vec >= nvec) return;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int w = 0; w < per && w * share < c; ++w) {
+    const Raw8<float> o{sums[warp + w][lane][0], sums[warp + w][lane][1]};
     float f[8];
     to_f32(o, f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] += f[k];
   }
-  griddep_wait();  // the zeros are written
+  griddep_wait();
   add_row8(dW + ((int64_t)row * nvec + vec) * 8, acc, scale, accumulate);
 }
 
@@ -550,7 +577,7 @@ bool embed_grad_is_few(int64_t T) { return T <= kFew; }
 
 cudaError_t launch_embed_grad_few(const EmbedIds& a, bool bf16, const void* dX, int d, float scale,
                                   bool accumulate, float* dW, cudaStream_t s) {
-  const dim3 grid((unsigned)a.T, (unsigned)((d + 255) / 256));
+  const dim3 grid((unsigned)a.T);
   auto launch = [&](auto kernel, auto* x) {
     // it reads ids and dX before its wait: behind the zeros only, whose launch waited for those
     if (!accumulate) return launch_behind(kernel, grid, 256, 0, s, a, x, d / 8, scale, accumulate, dW);

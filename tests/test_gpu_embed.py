@@ -351,3 +351,23 @@ def test_embed_grad_of_few_tokens_behind_another_call():
         he.embed_grad(ids, out, dW=dW, accumulate=True, sync=False)
         torch.cuda.synchronize()
         assert torch.equal(dW, ref)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [8, 264, 776, 1288, 2880])
+def test_embed_grad_of_few_tokens_by_how_often_a_row_occurs(d, dt):
+    """Rows of 1, 2, 3 ... tokens: the ways in which a row's work is shared out, with one slab of
+    columns and with many; up to and past the most tokens that go without a sort."""
+    g = torch.Generator().manual_seed(d)
+    often = [1, 2, 3, 4, 5, 6, 7, 8, 9, 11, 12, 13, 16, 17, 40, 64, 65, 150]
+    for T in (sum(often), 1023, 1024, 1025):
+        ids = torch.repeat_interleave(torch.arange(len(often), dtype=torch.int32), torch.tensor(often))
+        ids = torch.cat([ids, torch.full((T - len(ids),), 40, dtype=torch.int32)])
+        ids = ids[torch.randperm(T, generator=g)].cuda()
+        dX = torch.randn(T, d, generator=g).to(DT[dt]).cuda()
+        h = ckl.operator_handle(dX, V=41)
+        got = h.embed_grad(ids, dX, scale=3.0)
+        check_grad(got, ids, dX, 41, None, 3.0)
+        assert torch.equal(got, h.embed_grad(ids, dX, scale=3.0))
+        base = torch.randn(41, d, device="cuda")
+        check_grad(h.embed_grad(ids, dX, dW=base.clone(), accumulate=True), ids, dX, 41, None, 1.0, base)
