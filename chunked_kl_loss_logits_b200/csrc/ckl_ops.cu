@@ -299,7 +299,7 @@ ckl_status ckl_embed_grad(ckl_handle h, const int32_t* ids, const uint8_t* mask,
     uint64_t* a = reinterpret_cast<uint64_t*>(base + P.off_a);
     uint64_t* b = reinterpret_cast<uint64_t*>(base + P.off_b);
     float* part = reinterpret_cast<float*>(base + P.off_part);
-    const uint64_t* sorted = embed_sort_result(V) ? b : a;
+    const uint64_t* sorted = embed_sort_result(T, V) ? b : a;
     Launcher L{h, s};
     const int64_t n_fill = accumulate ? 0 : (int64_t)V * d;
     chk(L(KID_EMBED_SORT, 0, (double)T * 12 + 4.0 * n_fill, [&] {

@@ -9,8 +9,8 @@
 // writes the rows of the ids that occur. Atomic adds would read and write dW once per
 // token and make the sums' order, hence their last bits, change from run to run; instead
 // the tokens are sorted by (id, position) and each thread walks neighbouring sorted tokens
-// with eight columns of the running row sum in registers. A thousand tokens or fewer need no
-// sort: each compares itself with all.
+// with eight columns of the running row sum in registers. Some hundred tokens need no sort at
+// all, and of a few thousand each finds its place by comparing itself with all.
 #include <algorithm>
 
 #include "common.cuh"
@@ -63,6 +63,15 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedIds a, const T* _
   }
 }
 
+// Zeros for dW where it is overwritten: a block's share, 16 vectors of 16 bytes a thread.
+constexpr int kFill = 16;
+template <int THREADS>
+__device__ __forceinline__ void fill_zeros(float4* dst, int64_t n, int64_t block) {
+  const int64_t i0 = block * (THREADS * kFill), i1 = min(n, i0 + THREADS * kFill);
+#pragma unroll 8
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += THREADS) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
 // ------------------------------------------------------------------ sort
 // Stable least-significant-digit radix sort by one cluster of CTAs. Each of the cluster's
 // warps owns a contiguous range of the items, so "count per (digit, warp), prefix over
@@ -74,7 +83,6 @@ constexpr int kSortWarps = 32;
 constexpr int kBatch = 4;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxBins = 1 << kMaxDigitBits;
-constexpr int kFillBlock = 16384;  // 16-byte vectors of dW that a block zeroes
 constexpr size_t kSortSmem = (size_t)(kSortWarps * kMaxBins + 2 * kMaxBins + 32) * 4;
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -99,10 +107,7 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_launch_dependents();
   if (blockIdx.x >= cluster) {
-    const int64_t i0 = (int64_t)(blockIdx.x - cluster) * kFillBlock + tid;
-#pragma unroll 8
-    for (int64_t i = i0; i < min(n_fill, i0 - tid + kFillBlock); i += kSortWarps * 32)
-      fill[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    fill_zeros<kSortWarps * 32>(fill, n_fill, blockIdx.x - cluster);
     return;
   }
   uint32_t* hist = sm;                          // [warp][bin] counts, then places
@@ -216,6 +221,60 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
     else cluster_sync();
   }
   if (bad) atomicOr(a.status, (unsigned)ST_INDEX_RANGE);
+}
+
+// A few thousand tokens: every token's place is the number of tokens before it, those of smaller rows and
+// the earlier ones of its own, counted by comparing with all; a warp counts for four tokens. The whole
+// gradient of 2048 tokens of 512 columns takes 8.4 us so, 13.9 with the cluster's sort; 4096 11.7 and 16.7;
+// 6000, whose blocks no longer have an SM each, 17.7 and 18.4, 8192 21.5 and 19.7.
+constexpr int kRankMax = 4096;
+constexpr int kRankTokens = 32;  // of a block
+
+__global__ void __launch_bounds__(256)
+    embed_rank_kernel(const EmbedIds a, int blocks, uint64_t* out, float4* fill, int64_t n_fill) {
+  __shared__ uint4 keys[kRankMax / 4];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = (int)a.T;
+  griddep_launch_dependents();
+  if ((int)blockIdx.x >= blocks) {
+    fill_zeros<256>(fill, n_fill, blockIdx.x - blocks);
+    return;
+  }
+  uint32_t* key = reinterpret_cast<uint32_t*>(keys);
+  const int padded = (n + 127) / 128 * 128;
+  bool bad = false;
+#pragma unroll 4
+  for (int j = tid; j < padded; j += 256)  // past the last token: a key above every other
+    key[j] = j < n ? (uint32_t)row_of(a, a.ids[j], a.mask ? a.mask[j] : 1, bad) : ~0u;
+  if (bad && blockIdx.x == 0) atomicOr(a.status, (unsigned)ST_INDEX_RANGE);
+  __syncthreads();
+  const int i0 = (int)blockIdx.x * kRankTokens + warp * 4;
+  if (i0 >= n) return;
+  uint32_t mine[4], place[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int t = 0; t < 4; ++t) mine[t] = key[i0 + t];  // (padded: in bounds)
+  const int here = i0 / 128;  // the 128 tokens that hold these four
+  auto count = [&](int v, uint32_t more) {  // of 128 tokens, equal rows counted where more = 1
+    const uint4 k = keys[v * 32 + lane];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint32_t lim = mine[t] + more;
+      place[t] += (k.x < lim) + (k.y < lim) + (k.z < lim) + (k.w < lim);
+    }
+  };
+#pragma unroll 4
+  for (int v = 0; v < here; ++v) count(v, 1);
+#pragma unroll 4
+  for (int v = here + 1; v < padded / 128; ++v) count(v, 0);
+  const uint4 k = keys[here * 32 + lane];
+  const int j = here * 128 + lane * 4;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int i = i0 + t;
+    place[t] += (k.x < mine[t] + (j < i)) + (k.y < mine[t] + (j + 1 < i)) +
+                (k.z < mine[t] + (j + 2 < i)) + (k.w < mine[t] + (j + 3 < i));
+    place[t] = __reduce_add_sync(0xffffffffu, place[t]);
+    if (lane == t && i < n) out[place[t]] = (uint64_t)mine[t] << 32 | (uint32_t)i;
+  }
 }
 
 // ------------------------------------------------------------------ gradient
@@ -418,18 +477,17 @@ __global__ void __launch_bounds__(256)
 // have c CTAs: the one of the m-th takes the m-th of every c slabs of 256 columns. Its warps
 // take a slab each where it has many, or share one slab's tokens: each a contiguous part of them in
 // order of position, and the parts are added up in order. One launch instead of three, each of
-// which waits for the one before. d = 2880, added to dW, against the sort, in us: 64 tokens 3.0 and
-// 9.4, 256 3.7 and 10.9, 1024 7.0 and 16.0. Past 1024 the gain shrinks (2048 tokens 14.9 and 20.7, 4096
-// 35 and 29) and a row that takes every token costs ever more (1024 tokens 14.4 and 13.2, 2048 50
-// and 16.5).
-constexpr int kFew = 1024;
+// which waits for the one before. d = 2880, added to dW, against the places counted as below, in us:
+// 64 tokens 3.0 and 5.5, 256 3.6 and 5.7, 512 4.9 and 8.8; 512 tokens of one row 8.9 and 7.5. With 1024
+// tokens it still gains (7.0 and 9.8), but one row that takes them all costs 14.9 and 8.9.
+constexpr int kFew = 512;
 constexpr int kFewWords = kFew / 32;
 
 template <typename T>
 __global__ void __launch_bounds__(256)
     embed_grad_few_kernel(const EmbedIds a, const T* __restrict__ dX, int nvec, float scale,
                           bool accumulate, float* dW) {
-  static_assert(kFewWords == 32, "a word of the tokens' bits for each lane");
+  static_assert(kFewWords <= 32, "a word of the tokens' bits for each lane");
   __shared__ uint32_t has[kFewWords];  // bit j: token j has this row
   __shared__ uint16_t list[kFew];      // those tokens
   __shared__ float4 sums[8][32][2];
@@ -447,7 +505,7 @@ __global__ void __launch_bounds__(256)
     if (lane == 0) has[k * 8 + warp] = mine[k];
   }
   __syncthreads();
-  const uint32_t word = has[lane];
+  const uint32_t word = lane < kFewWords ? has[lane] : 0u;
   const uint32_t below = lane < i / 32 ? ~0u : lane > i / 32 ? 0u : (1u << (i & 31)) - 1u;
   const int m = (int)__reduce_add_sync(0xffffffffu, __popc(word & below));
   int upto = __popc(word);  // tokens in the words up to this lane's
@@ -509,12 +567,14 @@ __global__ void __launch_bounds__(256)
   add_row8(dW + ((int64_t)row * nvec + vec) * 8, acc, scale, accumulate);
 }
 
-__global__ void __launch_bounds__(1024) embed_zero_kernel(float4* dst, int64_t n) {
+__global__ void __launch_bounds__(256) embed_zero_kernel(float4* dst, int64_t n) {
   griddep_launch_dependents();
-  const int64_t i0 = (int64_t)blockIdx.x * kFillBlock + threadIdx.x;
-#pragma unroll 8
-  for (int64_t i = i0; i < min(n, i0 - threadIdx.x + kFillBlock); i += 1024)
-    dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  fill_zeros<256>(dst, n, blockIdx.x);
+}
+
+template <int THREADS>
+unsigned fill_blocks(int64_t n) {  // n floats
+  return (unsigned)((n / 4 + THREADS * kFill - 1) / (THREADS * kFill));
 }
 
 // Digits of the sort: bits of the largest key (V), in as few equal digits as fit the bins.
@@ -542,7 +602,8 @@ void launch_embed(const EmbedIds& a, bool bf16, const void* W, int d, float scal
                                                             scale, (uint16_t*)out);
 }
 
-int embed_sort_result(int32_t V) {
+int embed_sort_result(int64_t T, int32_t V) {
+  if (T <= kRankMax) return 0;
   int n_pass, bits;
   sort_digits(V, n_pass, bits);
   return n_pass % 2 == 0 ? 1 : 0;
@@ -550,6 +611,14 @@ int embed_sort_result(int32_t V) {
 
 cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_b, float* fill,
                               int64_t n_fill, cudaStream_t s) {
+  // Blocks of zeros, many more than fit at once, as not every SM gets as many (one block per SM with a
+  // fixed share: 58 us for 262 MB beside the sort of a cluster, this 41).
+  if (a.T <= kRankMax) {
+    const int blocks = (int)((a.T + kRankTokens - 1) / kRankTokens);
+    embed_rank_kernel<<<(unsigned)blocks + fill_blocks<256>(n_fill), 256, 0, s>>>(
+        a, blocks, buf_a, reinterpret_cast<float4*>(fill), n_fill / 4);
+    return cudaSuccess;
+  }
   int n_pass, bits;
   sort_digits(a.V, n_pass, bits);
   int cluster = 1;  // about a thousand items per CTA, at most the portable cluster size
@@ -563,11 +632,8 @@ cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_
   attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  // Blocks of zeros in whole clusters, many more than fit at once: where the GPU's parts do not
-  // divide into clusters some SMs hold fewer, so a fixed share for each would end late (a grid of
-  // one block per SM: 58 us for 262 MB, this 41).
-  const int64_t zero = (n_fill / 4 + kFillBlock - 1) / kFillBlock;
-  cfg.gridDim = dim3((unsigned)(cluster * (1 + (zero + cluster - 1) / cluster)), 1, 1);
+  const unsigned zero = fill_blocks<kSortWarps * 32>(n_fill);
+  cfg.gridDim = dim3((unsigned)cluster * (1 + (zero + cluster - 1) / cluster), 1, 1);
   cfg.blockDim = dim3(kSortWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = kSortSmem;
   cfg.stream = s;
@@ -593,8 +659,7 @@ cudaError_t launch_embed_grad_few(const EmbedIds& a, bool bf16, const void* dX, 
 }
 
 void launch_embed_zero(float* dst, int64_t n, cudaStream_t s) {
-  embed_zero_kernel<<<(unsigned)((n / 4 + kFillBlock - 1) / kFillBlock), 1024, 0, s>>>(
-      reinterpret_cast<float4*>(dst), n / 4);
+  embed_zero_kernel<<<fill_blocks<256>(n), 256, 0, s>>>(reinterpret_cast<float4*>(dst), n / 4);
 }
 
 // Lanes of a group: as many as a row has vectors of eight columns, or the most of 32, 16 and 8 that

@@ -24,7 +24,7 @@ void launch_embed(const EmbedIds& a, bool bf16, const void* W, int d, float scal
 // (row, position) of every token in ascending order, as row << 32 | position; the row is V for
 // tokens that have none here. The result is in `b` where embed_sort_result is 1, else in `a`.
 // The same launch zeroes n_fill floats (a multiple of 8) at `fill`.
-int embed_sort_result(int32_t V);
+int embed_sort_result(int64_t T, int32_t V);
 cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_b, float* fill,
                               int64_t n_fill, cudaStream_t s);
 // dW[row] (+)= scale * sum of the row's dX where that needs no sort (few tokens, by embed_grad_is_few).

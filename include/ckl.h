@@ -316,8 +316,8 @@ ckl_status ckl_embed_vocab_parallel(ckl_handle h, const ckl_vocab_group* group, 
  * takes subnormal numbers for zero). Tokens with mask 0, ids of
  * other ranks' rows and ids outside [0, V_total) (status CKL_ERR_INDEX_RANGE) add nothing.
  * Workspace: ckl_embed_grad_workspace_bytes, O(T): 16 T bytes and 3 (many tokens) to
- * 13 per cent of a bf16 dX (not touched for T <= 1024). A workspace serves one call at a time, here and below: two captured
- * graphs that may run at once need one each. */
+ * 13 per cent of a bf16 dX (not touched for T <= 512). A workspace serves one call at a time,
+ * here and below: two captured graphs that may run at once need one each. */
 ckl_status ckl_embed_grad_workspace_bytes(ckl_handle h, int64_t T, size_t* bytes);
 ckl_status ckl_embed_grad(ckl_handle h, const int32_t* ids, const uint8_t* mask, const void* dX,
                           int64_t T, int64_t V_total, int64_t v0, float scale, int accumulate,

@@ -360,7 +360,7 @@ def test_embed_grad_of_few_tokens_by_how_often_a_row_occurs(d, dt):
     columns and with many; up to and past the most tokens that go without a sort."""
     g = torch.Generator().manual_seed(d)
     often = [1, 2, 3, 4, 5, 6, 7, 8, 9, 11, 12, 13, 16, 17, 40, 64, 65, 150]
-    for T in (sum(often), 1023, 1024, 1025):
+    for T in (sum(often), 511, 512, 513, 1025):
         ids = torch.repeat_interleave(torch.arange(len(often), dtype=torch.int32), torch.tensor(often))
         ids = torch.cat([ids, torch.full((T - len(ids),), 40, dtype=torch.int32)])
         ids = ids[torch.randperm(T, generator=g)].cuda()
@@ -371,3 +371,56 @@ def test_embed_grad_of_few_tokens_by_how_often_a_row_occurs(d, dt):
         assert torch.equal(got, h.embed_grad(ids, dX, scale=3.0))
         base = torch.randn(41, d, device="cuda")
         check_grad(h.embed_grad(ids, dX, dW=base.clone(), accumulate=True), ids, dX, 41, None, 1.0, base)
+
+
+@pytest.mark.parametrize("T,V,hot", [
+    (1025, 3, 0), (1153, 70000, 0.3), (4000, 40, 0), (4095, 9000, 0.05),
+    (4096, 300000, 0.2),                       # the most tokens whose places are counted
+    (4097, 511, 0.1), (8193, 512, 0),          # sorted by digits: one of 9 bits, two of 5
+    (12345, 70000, 0.5), (20000, 1, 0),
+])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_embed_grad_by_both_ways_to_sort(T, V, hot, dt):
+    ids, mask, W, dX = case(T, 72, V, dt, masked=True, hot=hot)
+    ids[mask == 0] = 2 ** 31 - 1
+    dX[mask == 0] = float("nan")
+    clean = torch.where((mask != 0)[:, None], dX, torch.zeros_like(dX))
+    look = torch.where(mask != 0, ids, torch.zeros_like(ids))
+    h = ckl.operator_handle(W, V=V)
+    got = h.embed_grad(ids, dX, mask=mask, scale=0.7, dW=torch.full((V, 72), float("nan"), device="cuda"))
+    check_grad(got, look, clean, V, mask, float(np.float32(0.7)))
+    assert torch.equal(got, h.embed_grad(ids, dX, mask=mask, scale=0.7))
+    base = torch.randn(V, 72, device="cuda")
+    check_grad(h.embed_grad(ids, dX, mask=mask, dW=base.clone(), accumulate=True), look, clean, V,
+               mask, 1.0, base)
+
+
+@pytest.mark.parametrize("T", [3000, 9000])
+def test_an_id_out_of_range_among_many(T):
+    ids, _, W, dX = case(T, 64, 300, "bf16")
+    ids[T - 3] = 300
+    h = ckl.operator_handle(W, V=300)
+    dW = torch.empty(300, 64, device="cuda")
+    with pytest.raises(ckl.CKLError) as e:
+        h.embed_grad(ids, dX, dW=dW)
+    assert e.value.code == 4
+    keep = torch.ones(T, dtype=torch.uint8, device="cuda")
+    keep[T - 3] = 0
+    assert torch.equal(dW, h.embed_grad(ids, dX, mask=keep))
+
+
+def test_embed_grad_four_digits_of_many_tokens():
+    """A vocabulary of 28 bits and more tokens than have their places counted; whole numbers."""
+    V, T = 140_000_000, 8200
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    ids[::3] = V - 1
+    dX = torch.randint(-4, 5, (T, 8), generator=g, device="cuda").float()
+    h = ckl.ChunkedKL(V, 8, 1, dtype=torch.float32, max_chunk=1)
+    dW = h.embed_grad(ids, dX)
+    rows, back = torch.unique(ids, return_inverse=True)
+    want = torch.zeros(len(rows), 8, device="cuda").index_add_(0, back, dX)
+    assert torch.equal(dW[rows.long()], want)
+    dW[rows.long()] = 0
+    assert not dW.any()
+    h.close()
