@@ -480,6 +480,8 @@ __global__ void __launch_bounds__(256)
 // which waits for the one before. d = 2880, added to dW, against the places counted as below, in us:
 // 64 tokens 3.0 and 5.5, 256 3.6 and 5.7, 512 4.9 and 8.8; 512 tokens of one row 8.9 and 7.5. With 1024
 // tokens it still gains (7.0 and 9.8), but one row that takes them all costs 14.9 and 8.9.
+// Every thread waits for the launch before it, also where it writes nothing: a batch without a token
+// of these rows would otherwise be done before the zeros are, for all that follows it.
 constexpr int kFew = 512;
 constexpr int kFewWords = kFew / 32;
 
@@ -495,7 +497,10 @@ __global__ void __launch_bounds__(256)
   bool bad = false, ignore = false;
   const int32_t row = row_of(a, a.ids[i], a.mask ? a.mask[i] : 1, bad);
   if (bad && threadIdx.x == 0) atomicOr(a.status, (unsigned)ST_INDEX_RANGE);
-  if (row == a.V) return;
+  if (row == a.V) {
+    griddep_wait();
+    return;
+  }
   uint32_t mine[kFewWords / 8];
 #pragma unroll
   for (int k = 0; k < kFewWords / 8; ++k) {
@@ -515,7 +520,10 @@ __global__ void __launch_bounds__(256)
     if (lane >= o) upto += v;
   }
   const int c = __shfl_sync(0xffffffffu, upto, 31), slabs = (nvec + 31) / 32;
-  if (m >= slabs) return;
+  if (m >= slabs) {
+    griddep_wait();
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < kFewWords / 8; ++k) {
     const int before = __shfl_sync(0xffffffffu, upto - __popc(word), k * 8 + warp);
@@ -527,7 +535,7 @@ __global__ void __launch_bounds__(256)
   const int per = ns > 4 ? 1 : ns > 2 ? 2 : ns > 1 ? 4 : 8;  // warps for a slab
   const int group = warp / per, sub = warp % per, share = (c + per - 1) / per;
   const int p0 = min(c, sub * share), p1 = min(c, p0 + share);
-  bool wrote = false;
+  bool waited = false;
   for (int q = group; q < ns; q += 8 / per) {  // (at most one where warps share a slab)
     const int vec = (m + q * c) * 32 + lane;
     const bool on = vec < nvec;
@@ -546,15 +554,21 @@ __global__ void __launch_bounds__(256)
       sums[warp][lane][0] = r.a;
       sums[warp][lane][1] = r.b;
     } else if (on && sub == 0) {
-      if (!wrote) griddep_wait();  // the zeros are written
-      wrote = true;
+      if (!waited) griddep_wait();  // the zeros are written
+      waited = true;
       add_row8(dW + ((int64_t)row * nvec + vec) * 8, acc, scale, accumulate);
     }
   }
-  if (per == 1 || c == 1) return;
+  if (per == 1 || c == 1) {
+    if (!waited) griddep_wait();
+    return;
+  }
   __syncthreads();
   const int vec = (m + group * c) * 32 + lane;
-  if (sub != 0 || group >= ns || vec >= nvec) return;
+  if (sub != 0 || group >= ns || vec >= nvec) {
+    griddep_wait();
+    return;
+  }
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int w = 0; w < per && w * share < c; ++w) {
     const Raw8<float> o{sums[warp + w][lane][0], sums[warp + w][lane][1]};

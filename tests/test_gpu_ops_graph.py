@@ -80,3 +80,33 @@ def test_a_backward_pass_captured():
         W.grad = gain.grad = None
         step()
         assert torch.equal(W.grad, gW) and torch.equal(gain.grad, gg)
+
+
+@pytest.mark.parametrize("none", ["masked", "other rows"])
+@pytest.mark.parametrize("T", [1, 40, 512])
+def test_a_captured_gradient_without_a_token_is_read_by_the_next_node(T, none):
+    """An overwritten dW of 690 MB whose batch has no token here: the node after the call, which
+    depends on the call's last kernel alone, reads the zeros."""
+    rows, d = 60000, 2880
+    dX = torch.full((T, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ids = torch.randint(0, 1000, (T,), dtype=torch.int32, device="cuda")
+    mask = torch.zeros(T, dtype=torch.uint8, device="cuda") if none == "masked" else None
+    kw = {} if mask is not None else {"V_total": 1000 + rows, "v0": 1000}
+    h = ckl.operator_handle(dX, V=rows)
+    dW, seen = torch.empty(rows, d, device="cuda"), torch.empty(rows, d, device="cuda")
+    call = lambda: (h.embed_grad(ids, dX, mask=mask, dW=dW, sync=False, **kw), seen.copy_(dW))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(5):
+        dW.fill_(7.0)
+        seen.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert not seen.any() and not dW.any()
+    h.sync_status()
