@@ -91,12 +91,13 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
-// The two halves of a cluster barrier that orders no memory.
+// The two halves of a cluster barrier: what a thread read or wrote before it arrives is done for
+// those that have waited.
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // The first cluster sorts. The others (where dW is to be overwritten) zero dW meanwhile.
@@ -182,7 +183,8 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
         all += c;
       }
     }
-    // the other CTAs' counts are read: after the last pass nothing else keeps a CTA from leaving
+    // the other CTAs' counts are read: after the last pass nothing else keeps a CTA from leaving.
+    // The arrival releases, so that no read is still under way when the CTA it reads from leaves.
     const bool last = p == n_pass - 1;
     if (last) cluster_arrive();
     // exclusive prefix of `all` over the bins (threads past the bins hold 0)

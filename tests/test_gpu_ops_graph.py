@@ -110,3 +110,34 @@ def test_a_captured_gradient_without_a_token_is_read_by_the_next_node(T, none):
         torch.cuda.synchronize()
         assert not seen.any() and not dW.any()
     h.sync_status()
+
+
+@pytest.mark.parametrize("tokens", [4097, 6000, 20000])
+@pytest.mark.parametrize("rows", [400, 70000])
+def test_a_captured_gradient_whose_tokens_are_sorted(tokens, rows):
+    """More tokens than have their places counted, sorted by digits (one, and two): 4097 tokens leave
+    CTAs of the sort without any, which are done long before those whose counts they were asked for."""
+    gen = torch.Generator().manual_seed(tokens + rows)
+    ids = torch.randint(0, rows, (tokens,), generator=gen, dtype=torch.int32).cuda()
+    dX = torch.randint(-4, 5, (tokens, 40), generator=gen).to(torch.bfloat16).cuda()
+    h = ckl.operator_handle(dX, V=rows)
+    dW, ws = torch.empty(rows, 40, device="cuda"), h.embed_grad_workspace(tokens)
+    call = lambda: h.embed_grad(ids, dX, dW=dW, workspace=ws, sync=False)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for k in range(20):
+        ids.copy_(torch.randint(0, rows, (tokens,), generator=gen, dtype=torch.int32))
+        ids[::3] = k
+        dW.fill_(7.0)
+        ws.fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        want = torch.zeros(rows, 40, device="cuda").index_add_(0, ids, dX.float())
+        assert torch.equal(dW, want)  # whole numbers: every order of the sums is exact
+    h.sync_status()
