@@ -78,7 +78,9 @@ __device__ __forceinline__ void fill_zeros(float4* dst, int64_t n, int64_t block
 // digits, then over warps" gives every item its place, and equal keys keep their order.
 // The digit counts of the other CTAs are read from their shared memory. 32768 tokens, 18-bit
 // keys in two digits: 14 us, a chain of latencies (cluster barriers, counts of the others, the
-// scattered stores) rather than work; 16 CTAs instead of 8 take a tenth less.
+// scattered stores) rather than work. 16 CTAs take a tenth less (1.4 us of a call of 117), but a
+// cluster of more than 8 is a size that a kernel has to ask for and a device may refuse.
+constexpr int kSortCtas = 8;
 constexpr int kSortWarps = 32;
 constexpr int kBatch = 4;
 constexpr int kMaxDigitBits = 9;
@@ -102,13 +104,13 @@ __device__ __forceinline__ void cluster_wait() {
 
 // The first cluster sorts. The others (where dW is to be overwritten) zero dW meanwhile.
 __global__ void __launch_bounds__(kSortWarps * 32, 1)
-    embed_sort_kernel(const EmbedIds a, int n_pass, int bits, int cluster, uint64_t* buf_a,
-                      uint64_t* buf_b, float4* fill, int64_t n_fill) {
+    embed_sort_kernel(const EmbedIds a, int n_pass, int bits, uint64_t* buf_a, uint64_t* buf_b,
+                      float4* fill, int64_t n_fill) {
   extern __shared__ uint32_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_launch_dependents();
-  if (blockIdx.x >= cluster) {
-    fill_zeros<kSortWarps * 32>(fill, n_fill, blockIdx.x - cluster);
+  if (blockIdx.x >= kSortCtas) {
+    fill_zeros<kSortWarps * 32>(fill, n_fill, blockIdx.x - kSortCtas);
     return;
   }
   uint32_t* hist = sm;                          // [warp][bin] counts, then places
@@ -117,8 +119,8 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
   uint32_t* wsum = base + kMaxBins;             // [32]
   const int rank = (int)cluster_ctarank();
   const int bins = 1 << bits;
-  const int64_t per = ((a.T + (int64_t)cluster * kSortWarps * 32 - 1) /
-                       ((int64_t)cluster * kSortWarps * 32)) * 32;
+  constexpr int64_t kThreads = kSortCtas * kSortWarps * 32;
+  const int64_t per = (a.T + kThreads - 1) / kThreads * 32;
   const int64_t i0 = min(a.T, ((int64_t)rank * kSortWarps + warp) * per);
   const int64_t i1 = min(a.T, i0 + per);
   uint32_t* myhist = hist + warp * bins;
@@ -176,8 +178,8 @@ __global__ void __launch_bounds__(kSortWarps * 32, 1)
     cluster_sync();
     uint32_t before = 0, all = 0;
     if (tid < bins) {
-#pragma unroll 8
-      for (int r = 0; r < cluster; ++r) {
+#pragma unroll
+      for (int r = 0; r < kSortCtas; ++r) {
         const uint32_t c = ld_cluster_u32(cluster_map(tot + tid, (uint32_t)r));
         if (r < rank) before += c;
         all += c;
@@ -637,25 +639,23 @@ cudaError_t launch_embed_sort(const EmbedIds& a, uint64_t* buf_a, uint64_t* buf_
   }
   int n_pass, bits;
   sort_digits(a.V, n_pass, bits);
-  int cluster = 1;  // about a thousand items per CTA, at most the portable cluster size
-  while (cluster < 8 && (int64_t)cluster * 1024 < a.T) cluster *= 2;
   static std::atomic<uint64_t> attr_set{0};
   cudaError_t e = smem_once(embed_sort_kernel, kSortSmem, attr_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.x = kSortCtas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   const unsigned zero = fill_blocks<kSortWarps * 32>(n_fill);
-  cfg.gridDim = dim3((unsigned)cluster * (1 + (zero + cluster - 1) / cluster), 1, 1);
+  cfg.gridDim = dim3(kSortCtas * (1 + (zero + kSortCtas - 1) / kSortCtas), 1, 1);
   cfg.blockDim = dim3(kSortWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = kSortSmem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a, n_pass, bits, cluster, buf_a, buf_b,
+  return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a, n_pass, bits, buf_a, buf_b,
                             reinterpret_cast<float4*>(fill), n_fill / 4);
 }
 
