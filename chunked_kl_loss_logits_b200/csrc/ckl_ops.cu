@@ -80,8 +80,9 @@ ckl_status check_act8(const ckl_ctx* h, int64_t T, int64_t cols, int fmt, const 
   return CKL_OK;
 }
 
-// The contraction runs over `chunk` tokens at a time, so that the bf16 copy of the checkpoint
-// stays below kWgradChunkBytes whatever T is. (Chunks small enough to stay in L2, each unpacked
+// The contraction runs over `chunk` tokens at a time, so that the bf16 copy of the checkpoint, and
+// of fp32 handles each of the three bf16 parts of dY, stays below kWgradChunkBytes whatever T and n
+// are (or at kWgradChunkStep tokens, where so many alone are more). (Chunks small enough to stay in L2, each unpacked
 // behind the contraction of the one before, measured slower: 32768 x 2880 x 2880 in one chunk 586 us,
 // in chunks of 96 MB 603, of 48 MB 616: every contraction has its own start and end.)
 struct WgradPlan {
@@ -90,13 +91,14 @@ struct WgradPlan {
   size_t off_x = 0, off_parts = 0, off_sum = 0, total = 0;
 };
 
-constexpr int64_t kWgradChunkBytes = 256 << 20;  // of the bf16 copy
+constexpr int64_t kWgradChunkBytes = 256 << 20;  // of a bf16 copy
 constexpr int64_t kWgradChunkStep = 4096;        // tokens: whole accumulator ranges of the kernel
 
 WgradPlan wgrad_plan(const ckl_ctx* h, int64_t T, int64_t n, int64_t cols) {
   WgradPlan p;
   p.parts = h->dtype == CKL_BF16 ? 1 : 3;
-  const int64_t fit = kWgradChunkBytes / (cols * 2) / kWgradChunkStep * kWgradChunkStep;
+  const int64_t widest = p.parts > 1 ? std::max(n, cols) : cols;  // of the copies that are made
+  const int64_t fit = kWgradChunkBytes / (widest * 2) / kWgradChunkStep * kWgradChunkStep;
   p.chunk = std::max<int64_t>(1, std::min(T, std::max(fit, kWgradChunkStep)));
   p.n_split = wgrad_split(n, cols, p.parts * ((p.chunk + 63) / 64), h->num_sms);
   size_t o = 0;

@@ -5,6 +5,8 @@ is off only by the fp32 sums of its T terms (3 T for fp32): each addition, of wh
 cut or rounded, is off by at most one step, 2^-23 of the magnitudes summed so far; a few more for
 the partial results of token ranges and what was there before.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -183,3 +185,33 @@ def test_refusals():
     with pytest.raises(ckl.CKLError) as e:
         h.act8_weight_grad(dY, ckpt, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.code == 3
+
+
+@pytest.mark.parametrize("T,n,cols", [(32768, 201088, 1024), (400_000, 64000, 64), (1 << 22, 2880, 64),
+                                      (1 << 22, 64, 2880), (32768, 2880, 2880)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_the_workspace_is_bounded_whatever_the_tokens_and_outputs(T, n, cols, dt):
+    """A copy of X' and, for fp32, three parts of dY: 256 MB or 4096 tokens of each; the partial
+    results of at most 64 ranges where dW is small. (Sizes only: nothing is allocated.)"""
+    h = ckl.operator_handle(torch.empty(1, 8, dtype=DT[dt], device="cuda"))
+    size = ctypes.c_size_t()
+    assert ckl.lib().ckl_act8_weight_grad_workspace_bytes(h._h, T, n, cols, ctypes.byref(size)) == 0
+    copy = lambda width: max(256 << 20, 4096 * width * 2)
+    partial = 64 * n * cols * 4 if n * cols < 1 << 24 else 0
+    assert size.value <= copy(cols) + (3 * copy(n) if dt == "f32" else 0) + partial + 1024
+
+
+def test_fp32_layer_of_many_outputs_in_chunks():
+    """9000 tokens of 32768 outputs are contracted in three chunks, since the parts of dY take 192 KB
+    a token; small integers, so that every order of the sums is exact."""
+    T, n, cols = 9000, 32768, 64
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randint(-8, 9, (T, cols), generator=g, device="cuda").float()
+    dY = torch.randint(-4, 5, (T, n), generator=g, device="cuda").float()
+    h = ckl.operator_handle(x)  # (n is above a handle's largest d)
+    ckpt = h.act8_pack(x)
+    want = dY.double().t() @ x.double()
+    assert torch.equal(h.act8_weight_grad(dY, ckpt).double(), want)
+    base = torch.randint(-99, 99, (n, cols), generator=g, device="cuda").float()
+    got = h.act8_weight_grad(dY, ckpt, dW=base.clone(), accumulate=True)
+    assert torch.equal(got.double(), want + base.double())
