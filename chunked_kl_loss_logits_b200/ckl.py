@@ -853,13 +853,8 @@ class _EmbeddingFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, g):
         ids, mask = ctx.saved_tensors
-        dW = None
-        if ctx.needs_input_grad[0]:
-            dW = ctx.handle.embed_grad(ids, g.contiguous(), mask, ctx.scale,
-                                       sync=ctx.check).to(ctx.w_dtype)
-        elif ctx.check:
-            ctx.handle.sync_status()
-        return dW, None, None, None, None, None
+        dW = ctx.handle.embed_grad(ids, g.contiguous(), mask, ctx.scale, sync=ctx.check)
+        return dW.to(ctx.w_dtype), None, None, None, None, None
 
 
 def embedding(ids, W, mask=None, scale: float = 1.0, handle: ChunkedKL | None = None,
@@ -867,12 +862,19 @@ def embedding(ids, W, mask=None, scale: float = 1.0, handle: ChunkedKL | None = 
     """Autograd-friendly scale * W[ids] (zeros, and no gradient, for tokens with mask 0). W's
     gradient is formed in fp32 by sorted tokens and does not change from run to run.
 
-    check=True: backward() waits and raises CKLError if an id was outside [0, V); check=False:
-    nothing waits and the status stays in the handle (operator_handle(W, W.shape[0])), as a step
-    captured in a CUDA graph needs. Before that capture, as with any operator: run the step once on
-    a side stream, and let go of whatever still holds an eager graph of the same leaves."""
+    check=True: CKLError if an id was outside [0, V), raised by backward(), which waits, or by this
+    call, which waits then, where W gets no gradient (grad mode off or a frozen W); only a call
+    captured in a CUDA graph waits for nothing. Until a call has waited, the status of an id out of
+    range stays in the handle (operator_handle(W, W.shape[0])), whose next waiting call raises it.
+    check=False: nothing waits, as a step captured in a CUDA graph needs, and handle.sync_status()
+    tells. Before that capture, as with any operator: run the step once on a side stream, and let go
+    of whatever still holds an eager graph of the same leaves."""
     if handle is None:
         handle = operator_handle(W, W.shape[0])
+    if check and not (torch.is_grad_enabled() and W.requires_grad):  # no backward pass to tell
+        with torch.cuda.device(handle._index):
+            capturing = torch.cuda.is_current_stream_capturing()
+        return handle.embed(ids, W.detach(), mask, scale, sync=not capturing)
     return _EmbeddingFn.apply(W, ids, mask, scale, handle, check)
 
 

@@ -424,3 +424,43 @@ def test_embed_grad_four_digits_of_many_tokens():
     dW[rows.long()] = 0
     assert not dW.any()
     h.close()
+
+
+@pytest.mark.parametrize("frozen", [False, True])
+def test_autograd_embedding_without_a_gradient_reports_ids_out_of_range(frozen):
+    """No backward pass will tell: the lookup itself waits and raises, and leaves no status that a later
+    call with right ids would raise."""
+    ids, mask, W, _ = case(40, 64, 31, "bf16", masked=True)
+    W.requires_grad_(not frozen)
+    wild = ids.clone()
+    wild[mask.nonzero()[0]] = 31
+    with torch.set_grad_enabled(frozen):
+        with pytest.raises(ckl.CKLError) as e:
+            ckl.embedding(wild, W, mask=mask)
+        assert e.value.code == 4
+        out = ckl.embedding(ids, W, mask=mask)
+        assert not out.requires_grad
+        assert torch.equal(out, ckl.operator_handle(W, V=31).embed(ids, W, mask=mask))
+        quiet = ckl.embedding(wild, W, mask=mask, check=False)  # nothing waits: the status stays
+    assert not quiet[mask.nonzero()[0]].any()
+    with pytest.raises(ckl.CKLError):
+        ckl.operator_handle(W, V=31).sync_status()
+
+
+def test_autograd_embedding_without_a_gradient_in_a_capture():
+    """What is captured waits for nothing, whatever `check` says; the status is there to ask for."""
+    ids, _, W, _ = case(40, 64, 31, "bf16")
+    with torch.no_grad():
+        want = ckl.embedding(ids, W)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = ckl.embedding(ids, W)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    ids[3] = 31
+    g.replay()
+    torch.cuda.synchronize()
+    assert not out[3].any()
+    with pytest.raises(ckl.CKLError):
+        ckl.operator_handle(W, V=31).sync_status()
