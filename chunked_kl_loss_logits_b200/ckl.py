@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import importlib.machinery
 import importlib.util
 import os
@@ -121,7 +122,9 @@ def lib() -> ctypes.CDLL:
                                  ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
-        f = getattr(L, name)
+        f = getattr(L, name, None)
+        if f is None:  # an older build: the calls that it has still work
+            continue
         f.argtypes = args
         f.restype = res
     _lib = L
@@ -244,15 +247,18 @@ def _ops():
         if not os.path.exists(OPS_PATH):
             raise RuntimeError(f"{OPS_PATH} is missing: build it with "
                                "`python -m chunked_kl_loss_logits_b200.build`")
+        L = lib()
+        try:
+            calls = [getattr(L, "ckl_" + f) for f in (
+                "embed", "embed_grad_workspace_bytes", "embed_grad", "act8_pack", "act8_unpack",
+                "act8_weight_grad_workspace_bytes", "act8_weight_grad", "norm",
+                "norm_bwd_workspace_bytes", "norm_bwd")]
+        except AttributeError as e:
+            raise RuntimeError(f"{LIB_PATH} is a build without these operators") from e
         loader = importlib.machinery.ExtensionFileLoader("_ckl_ops", OPS_PATH)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_ckl_ops", loader))
         loader.exec_module(m)
-        L = lib()
-        m.bind(CKLError, tuple(
-            ctypes.cast(getattr(L, "ckl_" + f), ctypes.c_void_p).value
-            for f in ("embed", "embed_grad_workspace_bytes", "embed_grad", "act8_pack",
-                      "act8_unpack", "act8_weight_grad_workspace_bytes", "act8_weight_grad", "norm",
-                      "norm_bwd_workspace_bytes", "norm_bwd")))
+        m.bind(CKLError, tuple(ctypes.cast(f, ctypes.c_void_p).value for f in calls))
         _ops_module = m
     return _ops_module
 
@@ -339,7 +345,7 @@ class ChunkedKL:
         _check(lib().ckl_create(ctypes.byref(h), dev.index or 0,
                                 F32 if dtype == torch.float32 else BF16, V, d, K, max_chunk),
                "ckl_create")
-        self._h, self._index, self._ops = h, dev.index or 0, _ops()
+        self._h, self._index = h, dev.index or 0
         self._ctx = (h.value, V, d, dtype == torch.bfloat16, self._index)
 
     def close(self):
@@ -578,6 +584,10 @@ class ChunkedKL:
     # Checks, allocations and the call are made in csrc/torch_ops.cpp. Tensors must be dense, of the
     # handle's dtype and on its device; `stream` (by default the current one) is where the call
     # runs and what it allocates is allocated. A call captured in a CUDA graph takes sync=False.
+    @functools.cached_property
+    def _ops(self):  # at the first of these calls: the loss needs libckl.so alone
+        return _ops()
+
     @contextlib.contextmanager
     def _on(self, stream):
         if stream.device.index != self._index:

@@ -87,3 +87,29 @@ def test_rms_norm_refuses_strided_inputs():
         ckl.rms_norm(x[:, ::2], g, handle=object())
     with pytest.raises(ValueError):
         ckl.rms_norm(torch.zeros(4, 8), g, residual=torch.zeros(3, 8), handle=object())
+
+
+class _OlderLibrary:
+    """A build of the library from before the operators: it creates handles, and has the loss."""
+
+    def __init__(self, path):
+        for f in ckl.header_functions():
+            if not any(w in f for w in ("embed", "act8", "norm")):
+                setattr(self, f, lambda *a: 0)
+
+
+def test_the_loss_needs_neither_the_module_nor_a_library_with_the_operators(monkeypatch):
+    monkeypatch.setattr(ckl, "_ops_module", None)
+    monkeypatch.setattr(ckl, "_lib", None)
+    monkeypatch.setattr(ckl, "LIB_PATH", __file__)
+    monkeypatch.setattr(ckl.ctypes, "CDLL", _OlderLibrary)
+    x = torch.zeros(2, 8)
+    h = ckl.ChunkedKL(16, 8, 4, dtype=torch.float32, max_chunk=8, device="cuda:0")
+    assert h.workspace_bytes(2, 2) == 0
+    with pytest.raises(RuntimeError, match="without these operators"):
+        h.act8_pack(x)
+    monkeypatch.setattr(ckl, "OPS_PATH", "/nowhere/_ckl_ops.so")
+    h = ckl.ChunkedKL(16, 8, 4, dtype=torch.float32, max_chunk=8, device="cuda:0")
+    with pytest.raises(RuntimeError, match="is missing"):
+        h.act8_pack(x)
+    h.close()
