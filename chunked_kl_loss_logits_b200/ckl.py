@@ -843,7 +843,9 @@ def operator_handle(t, V: int = 1) -> ChunkedKL:
     d = t.shape[-1]
     key = (index, t.dtype, V, d)
     try:
-        return _OP_HANDLES.handles[key]
+        h = _OP_HANDLES.handles[key]
+        if h._h:  # not closed by who had it before
+            return h
     except AttributeError:
         _OP_HANDLES.handles = {}
     except KeyError:

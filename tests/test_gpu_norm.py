@@ -402,3 +402,14 @@ def test_refusals():
             bad()
         codes.append(e.value.code)
     assert codes == [1, 1, 1, 2, 3, 7]
+
+
+def test_a_cached_handle_that_was_closed_is_replaced():
+    x = torch.randn(4, 72, device="cuda")
+    g = torch.ones(72, device="cuda")
+    want = ckl.rms_norm(x, g)
+    h = ckl.operator_handle(x)
+    h.close()
+    with pytest.raises(ckl.CKLError):
+        h.norm(x, g)
+    assert torch.equal(ckl.rms_norm(x, g), want)

@@ -1,6 +1,7 @@
 """Checks of the operators around the loss that need no GPU: null handles, and what the
 Python side refuses before it calls the library."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -113,3 +114,26 @@ def test_the_loss_needs_neither_the_module_nor_a_library_with_the_operators(monk
     with pytest.raises(RuntimeError, match="is missing"):
         h.act8_pack(x)
     h.close()
+
+
+def test_operator_handle_replaces_a_closed_one(monkeypatch):
+    class Handle:
+        def __init__(self, *a, **k):
+            self._h = object()
+
+        def close(self):
+            self._h = None
+
+    class OnGpu:
+        dtype, shape, device = torch.float32, (4, 8), torch.device("cuda", 0)
+
+        def get_device(self):
+            return 0
+
+    monkeypatch.setattr(ckl, "ChunkedKL", Handle)
+    monkeypatch.setattr(ckl, "_OP_HANDLES", threading.local())
+    a = ckl.operator_handle(OnGpu())
+    assert ckl.operator_handle(OnGpu()) is a
+    a.close()
+    b = ckl.operator_handle(OnGpu())
+    assert b is not a and b._h and ckl.operator_handle(OnGpu()) is b
