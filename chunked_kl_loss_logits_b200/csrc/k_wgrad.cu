@@ -4,8 +4,9 @@
 //
 // on the tensor cores. X' has at most 8 significant bits, so bf16 holds it exactly: it is
 // unpacked to a bf16 workspace first. bf16 dY enters as it is; fp32 dY is cut into three bf16
-// parts of 8 bits each (their sum is dY exactly) that are contracted one after the other, so
-// both types get exact products and fp32 sums.
+// parts of 8 bits each that are contracted one after the other, so both types get exact products
+// and fp32 sums. (The parts add up to dY exactly from 2^-110 on; of a smaller number they leave out
+// what lies below bf16's smallest, 2^-133.)
 //
 // Bound by the tensor cores: 2 T n c operations (three times that for fp32) against T (2n + c)
 // bytes, a thousand operations a byte at n = c = 2880.
@@ -295,7 +296,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 }
 
 // fp32 -> three bf16 parts, cut (not rounded) after 8 significant bits each, so that they add
-// up to the value exactly and none overflows; the part of the lowest bits first.
+// up to the value exactly (but for bits below 2^-133) and none overflows; the part of the lowest
+// bits first.
 __global__ void __launch_bounds__(256) split3_kernel(const float* __restrict__ x, int64_t n8,
                                                      uint16_t* __restrict__ out) {
   griddep_launch_dependents();

@@ -215,3 +215,20 @@ def test_fp32_layer_of_many_outputs_in_chunks():
     base = torch.randint(-99, 99, (n, cols), generator=g, device="cuda").float()
     got = h.act8_weight_grad(dY, ckpt, dW=base.clone(), accumulate=True)
     assert torch.equal(got.double(), want + base.double())
+
+
+def test_how_far_down_fp32_gradients_keep_all_their_bits():
+    """bf16 ends at 2^-133, the lowest bit of a number from 2^-110 on: from there the three parts add
+    up to dY, and below they leave out less than 2^-133 of it. One token, times 2^40."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    frac = 1 + (2 * torch.randint(0, 1 << 22, (1, 512), generator=g, device="cuda") + 1).double() * 2.0 ** -23
+    sign = 1 - 2 * torch.randint(0, 2, (1, 512), generator=g, device="cuda").double()
+    x = torch.full((1, 32), 2.0 ** 40, device="cuda")
+    h = ckl.operator_handle(x)
+    ckpt = h.act8_pack(x)
+    for low, high, left_out in ((-110, -90, 0.0), (-126, -110, 2.0 ** -133)):
+        exponent = torch.randint(low, high, (1, 512), generator=g, device="cuda").double()
+        exponent[0, 0] = low
+        dY = (sign * frac * torch.exp2(exponent)).float()
+        got = h.act8_weight_grad(dY, ckpt).double()
+        assert bool(((got - dY.double().t() * 2.0 ** 40).abs() <= left_out * 2.0 ** 40).all())
