@@ -413,3 +413,46 @@ def test_a_cached_handle_that_was_closed_is_replaced():
     with pytest.raises(ckl.CKLError):
         h.norm(x, g)
     assert torch.equal(ckl.rms_norm(x, g), want)
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 40), ("f32", 136), ("f32", 520), ("f32", 2880), ("f32", 4104),
+                                  ("f32", 8192), ("f32", 12000), ("bf16", 40), ("bf16", 1032),
+                                  ("bf16", 4104), ("bf16", 8192), ("bf16", 12000), ("bf16", 24000)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_blocks_that_walk_several_rows(dt, d, residual):
+    """Every count of vectors a lane and of rows ahead, refilled several times: against the formulas
+    in 64 bits, against the same rows in a call of their own (a row a block), and in place."""
+    T = 8003 if d <= 136 else 4001 if d <= 1032 else 1203
+    x, dY = rows(T, d, dt), rows(T, d, dt, 2)
+    r, dS = (rows(T, d, dt, 1), rows(T, d, dt, 3)) if residual else (None, None)
+    gain = (1 + 0.2 * torch.randn(d, device="cuda")).to(DT[dt])
+    h, eps, half = ckl.operator_handle(x), 1e-3, torch.finfo(DT[dt]).eps / 2
+    y, s, c = h.norm(x, gain, residual=r, eps=eps)
+    dX, dg = h.norm_bwd(dY, c, gain, d_residual=dS)
+
+    s64, g64, dY64 = s.double(), gain.double(), dY.double()
+    rstd = 1 / (s64.square().mean(1, keepdim=True) + float(np.float32(eps))).sqrt()
+    want = s64 * rstd * g64
+    assert bool(((y.double() - want).abs() <= (half + 1.01 * (d / 2 + 6) * U) * want.abs()).all())
+    kept = ckl.operator_handle(torch.empty(1, 8, device="cuda")).act8_unpack(c).double()
+    hat, a = kept * rstd, dY64 * g64
+    p = 0.0 if dS is None else dS.double()
+    wX = rstd * (a - hat * (a * hat).mean(1, keepdim=True)) + p
+    mag = rstd * (a.abs() + hat.abs() * (a * hat).abs().mean(1, keepdim=True)) + abs(p)
+    assert bool(((dX.double() - wX).abs() <= half * wX.abs() + 1.01 * (2 * d + 24) * U * mag).all())
+    wg, magG = (dY64 * hat).sum(0), (dY64 * hat).abs().sum(0)
+    assert bool(((dg.double() - wg).abs() <= 1.01 * (T + d / 2 + 12) * U * magG).all())
+
+    few = torch.tensor([0, 1, 700, T // 2, T - 2, T - 1], device="cuda")
+    at = lambda t: None if t is None else t[few].contiguous()
+    y1, s1, c1 = h.norm(at(x), gain, residual=at(r), eps=eps)
+    assert torch.equal(y[few], y1) and torch.equal(s[few], s1) and torch.equal(c.rstd[few], c1.rstd)
+    assert torch.equal(c.q[few], c1.q) and torch.equal(c.scale[few], c1.scale)
+    assert torch.equal(dX[few], h.norm_bwd(at(dY), c1, gain, d_residual=at(dS))[0])
+
+    x2, r2, c2 = x.clone(), None if r is None else r.clone(), h.act8_empty(T, d, rstd=True)
+    h.norm(x2, gain, residual=r2, eps=eps, out=(x2, r2, c2))
+    assert torch.equal(x2, y) and (r is None or torch.equal(r2, s)) and torch.equal(c2.q, c.q)
+    dY2 = dY.clone()
+    _, dg2 = h.norm_bwd(dY2, c2, gain, d_residual=dS, dX=dY2)
+    assert torch.equal(dY2, dX) and torch.equal(dg2, dg)

@@ -232,3 +232,24 @@ def test_how_far_down_fp32_gradients_keep_all_their_bits():
         dY = (sign * frac * torch.exp2(exponent)).float()
         got = h.act8_weight_grad(dY, ckpt).double()
         assert bool(((got - dY.double().t() * 2.0 ** 40).abs() <= left_out * 2.0 ** 40).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_relative_error_over_many_tokens(dt):
+    """The bound of the other cases grows with the tokens; the error must not. The tensor cores cut
+    a running sum after each 16 tokens, and an accumulator runs over 1024. A cut takes on average
+    0.72 2^-24 of the sum (half a step of it, which is 2^-24 to 2^-23 of the value). Terms of random
+    sign make the 64 sums of a run a random walk: their own sum is 64^1.5 / 3^0.5 of a step of the walk,
+    the last one 8, so the cuts take 37 * 0.72 * 2^-24 = 1.6e-6 of the result, and the 32 runs' sums in
+    registers, rounded, some 2^-24. (One accumulator over all the tokens: 181 / 8 times that.) The
+    layer is large enough that no range of tokens is split off."""
+    T, n, cols = 32768, 2880, 2880
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(T, cols, generator=g, device="cuda").to(DT[dt])
+    dY = torch.randn(T, n, generator=g, device="cuda").to(DT[dt])
+    h = ckl.operator_handle(x)
+    ckpt = h.act8_pack(x)
+    want = dY.double().t() @ h.act8_unpack(ckpt).double()
+    rel = float((h.act8_weight_grad(dY, ckpt).double() - want).norm() / want.norm())
+    print(dt, f"{rel:.2e}")
+    assert rel <= 2e-6
