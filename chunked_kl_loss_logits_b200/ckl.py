@@ -928,6 +928,8 @@ def rms_norm(x, gain, residual=None, eps: float = 1e-5, fmt: str = "int8",
     if not x.is_contiguous() or (residual is not None and
                                  (not residual.is_contiguous() or residual.shape != x.shape)):
         raise ValueError("x and residual must be contiguous tensors of one shape")
+    if x.dim() == 0 or x.shape[-1] != handle.d:
+        raise ValueError("x's last dimension must be the handle's d")
     return _RmsNormFn.apply(x, gain, residual, eps, fmt, handle)
 
 

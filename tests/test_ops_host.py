@@ -137,3 +137,15 @@ def test_operator_handle_replaces_a_closed_one(monkeypatch):
     a.close()
     b = ckl.operator_handle(OnGpu())
     assert b is not a and b._h and ckl.operator_handle(OnGpu()) is b
+
+
+def test_rms_norm_refuses_a_handle_of_another_width():
+    """16 columns are not two rows of 8."""
+    class Handle:
+        d = 8
+
+        def norm(self, *a):
+            raise AssertionError("called")
+
+    with pytest.raises(ValueError):
+        ckl.rms_norm(torch.zeros(4, 16), torch.ones(8), handle=Handle())
