@@ -83,8 +83,9 @@ ckl_status check_act8(const ckl_ctx* h, int64_t T, int64_t cols, int fmt, const 
 // The contraction runs over `chunk` tokens at a time, so that the bf16 copy of the checkpoint, and
 // of fp32 handles each of the three bf16 parts of dY, stays below kWgradChunkBytes whatever T and n
 // are (or at kWgradChunkStep tokens, where so many alone are more). (Chunks small enough to stay in L2, each unpacked
-// behind the contraction of the one before, measured slower: 32768 x 2880 x 2880 in one chunk 586 us,
-// in chunks of 96 MB 603, of 48 MB 616: every contraction has its own start and end.)
+// behind the contraction of the one before, measured slower: 32768 x 2880 x 2880 in one chunk 478 us
+// from a cool start and 560 under the power limit, in chunks of 96 MB 487 and 571, of 48 MB 502 and
+// 592: every contraction has its own start and end.)
 struct WgradPlan {
   int64_t chunk = 0, parts = 0;
   int n_split = 1;

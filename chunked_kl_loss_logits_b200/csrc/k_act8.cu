@@ -89,17 +89,23 @@ __global__ void __launch_bounds__(256)
 // The norm kernels: a block of WPR warps walks rows in steps of the grid, each lane with VPT
 // vectors of eight columns. What it needs of the rows ahead is on its way to shared memory
 // (cp.async, each thread its own vectors, so that nothing but the row sum is synchronised): two
-// rows, as four keep fewer blocks on an SM (272 us against 275 for both passes below).
+// rows, as four keep fewer blocks on an SM (272 us against 275 for both passes below; 4096 x 2048
+// without a residual, forward: two rows 11.0 us, three 11.4, four 12.0).
 // 32768 x 2880 bf16 with a residual: forward 148 us (5.75 TB/s), backward 121 us (5.5 TB/s). Rows in
 // registers alone, several to a block, took 173 and 215 us: the sums of dg leave room for too few
 // warps to keep HBM busy without copies under way. Asking L2 for the scales of the rows ahead
-// cost 8 us.
+// cost 8 us. Rows of 4 or 7 vectors a lane (above 8192 columns) spill registers, 24 to 172 bytes
+// forward and 108 to 700 backward: 8192 bf16 rows with a residual run backward at 5.6 TB/s at 8192 columns,
+// 4.2 at 16384 and 1.9 at 24000, forward at 5.3, 5.4 and 4.7.
 template <typename T, int WPR, int VPT, bool BWD>
 struct NormCfg {
   static constexpr int kThreads = WPR * 32;
   // Blocks per SM, in warps: 36 forward, 24 backward, whose sums of dg are in registers; 32 where a
-  // power of two fills them at one vector a lane (d = 4096: 79 us for 15 thousand rows against 91;
-  // rows of 6 or 12 warps lose 3% that way).
+  // power of two fills them at one vector a lane. 64 million elements backward with d_sum, in us with
+  // 32 and with 24 warps: bf16 d = 256 96 and 95, 512 87 and 85, 1024 84 and 82, 2048 85 and 84,
+  // 4096 87 and 99; fp32 137, 162, 173, 169, 138 and 137, 160, 170, 164, 152. So it gains at 16 warps a
+  // row (d = 4096) and costs 1 to 3% below, without d_sum up to 8% (fp32 d = 512: 13%); rows of 6 or
+  // 12 warps lose 3%.
   static constexpr bool kEven = VPT == 1 && (WPR & (WPR - 1)) == 0;
   static constexpr int kWant = (!BWD ? 36 : kEven ? 32 : 24) / WPR;
   static constexpr int kPerSm = kWant < 1 ? 1 : kWant > 16 ? 16 : kWant;

@@ -77,8 +77,8 @@ __device__ __forceinline__ void fill_zeros(float4* dst, int64_t n, int64_t block
 // warps owns a contiguous range of the items, so "count per (digit, warp), prefix over
 // digits, then over warps" gives every item its place, and equal keys keep their order.
 // The digit counts of the other CTAs are read from their shared memory. 32768 tokens, 18-bit
-// keys in two digits: 14 us, a chain of latencies (cluster barriers, counts of the others, the
-// scattered stores) rather than work. 16 CTAs take a tenth less (1.4 us of a call of 117), but a
+// keys in two digits: 14 us, for this plan a chain of latencies (cluster barriers, counts of the others,
+// the scattered stores) on 8 of the SMs rather than work. 16 CTAs take a tenth less (1.4 us of a call of 117), but a
 // cluster of more than 8 is a size that a kernel has to ask for and a device may refuse.
 constexpr int kSortCtas = 8;
 constexpr int kSortWarps = 32;

@@ -2,7 +2,8 @@
 //
 //     dW[n][c] (+)= sum_t dY[t][n] X'[t][c],    X'[t][c] = code[t][c] * 2^e[t][c / 32]
 //
-// on the tensor cores. X' has at most 8 significant bits, so bf16 holds it exactly: it is
+// on the tensor cores. X' has at most 8 significant bits, so bf16 holds it exactly (from 2^-126
+// on; below that to 2^-134): it is
 // unpacked to a bf16 workspace first. bf16 dY enters as it is; fp32 dY is cut into three bf16
 // parts of 8 bits each that are contracted one after the other, so both types get exact products
 // and fp32 sums. (The parts add up to dY exactly from 2^-110 on; of a smaller number they leave out
@@ -26,9 +27,12 @@
 // Every wait is bounded (common.cuh).
 //
 // Converting the codes inside the contraction (by further warps, from the codes in shared
-// memory or in registers) was measured and not kept: 560 us at 32768 x 2880 x 2880. The
-// extra passes over shared memory (codes in and out, bf16 in) take bandwidth that the MMA
-// needs for its operands; unpacking first moves 3 bytes a code through HBM and L2 instead.
+// memory or in registers) was measured and not kept: 570 us and more at 32768 x 2880 x 2880, where
+// unpacking first took 488 then, both over 25 calls from a cool start (477 now; 560 under the power
+// limit, at which the two were not compared). The extra passes over shared memory (codes in and
+// out, bf16 in) take bandwidth that the MMA needs for its operands; unpacking first moves 3 bytes a
+// code through HBM and L2 instead. The epilogue's 128 sums a thread leave the 168 registers short
+// by 24 bytes, which are spilled.
 #include <algorithm>
 #include <atomic>
 
