@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(256)
 // take a slab each where it has many, or share one slab's tokens: each a contiguous part of them in
 // order of position, and the parts are added up in order. One launch instead of three, each of
 // which waits for the one before. d = 2880, added to dW, against the places counted as below, in us:
-// 64 tokens 3.0 and 5.5, 256 3.6 and 5.7, 512 4.9 and 8.8; 512 tokens of one row 8.9 and 7.5. With 1024
+// 64 tokens 3.0 and 5.5, 256 3.6 and 5.7, 512 4.9 and 8.8; 512 tokens of one row 7.8 and 7.5. With 1024
 // tokens it still gains (7.0 and 9.8), but one row that takes them all costs 14.9 and 8.9.
 // Every thread waits for the launch before it, also where it writes nothing: a batch without a token
 // of these rows would otherwise be done before the zeros are, for all that follows it.

@@ -344,8 +344,7 @@ ckl_status ckl_act8_unpack(ckl_handle h, const void* q, const uint8_t* scale, in
  * dW: n x cols fp32, added to with accumulate != 0 and overwritten otherwise. Products are
  * exact and summed in fp32 (fp32 dY as three bf16 parts that add up to it from 2^-110 on and
  * leave out what lies below 2^-133 of smaller numbers; X' below 2^-126 as bf16 rounds it).
- * T < 2^29. Runs on
- * the tensor cores of sm_100a, in chunks of tokens where T is large. Workspace:
+ * T < 2^29. Runs on the tensor cores of sm_100a, in chunks of tokens where T is large. Workspace:
  * ckl_act8_weight_grad_workspace_bytes (a bf16 copy of a chunk of X', for fp32 three of a chunk
  * of dY, each at most 256 MB or 4096 tokens, whichever is more, and a partial dW for each range
  * of tokens where n x cols alone does not fill the GPU). */
